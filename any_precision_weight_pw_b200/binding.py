@@ -25,7 +25,8 @@ EXPORTED = ["pw_moe_create", "pw_set_block_bits", "pw_moe_forward", "pw_destroy"
             "pw_forward_launches", "pw_plane_bytes", "pw_repack_planes", "pw_route_static",
             "pw_get_forward_bits", "pw_set_switch_lag", "pw_routing_stats", "pw_plan_release",
             "pw_enable_paging", "pw_resident_bytes", "pw_workspace_bytes", "pw_compact_pages",
-            "pw_last_error", "pw_abi_version", "pw_route_geometry"]
+            "pw_last_error", "pw_abi_version", "pw_route_geometry", "pw_add_rms_norm",
+            "pw_token_logprobs", "pw_adapters", "pw_moe_forward_norm"]
 
 
 class PwError(RuntimeError):
@@ -91,6 +92,13 @@ def lib():
         L.pw_repack_planes.argtypes = [P, P, i32, i32, i32, P]
         L.pw_route_static.argtypes = [P, P, P, i32, i32, i32, i32, i32, P, P, P]
         L.pw_route_geometry.argtypes = [i32, i32, i32, i32, C.POINTER(C.c_int64)]
+        i64 = C.c_int64
+        L.pw_add_rms_norm.argtypes = [P, i32, i64, P, i32, i64, P, i32, C.c_float, i32, i32, P,
+                                      i64, P, i32, i64, P, i32, P]
+        L.pw_token_logprobs.argtypes = [P, i32, i64, i32, i32, P, i32, P, P, P, P, P]
+        L.pw_adapters.argtypes = [P, i64, P, P, P, P, P, i32, i32, i32, i32, i32, P, i64, P, i32,
+                                  i64, P]
+        L.pw_moe_forward_norm.argtypes = [P, P, P, P, C.c_float, i32, P, P, P, P, P]
         L.pw_last_error.restype = C.c_char_p
         L.pw_abi_version.restype = i32
         for name in EXPORTED:
@@ -132,11 +140,14 @@ def repack_planes(planes, cols: int, stream=None):
     return out
 
 
-def linear(planes, lut, bits: int, x, rows: int, y=None, stream=None):
+def linear(planes, lut, bits: int, x, rows: int, y=None, stream=None, adapters=None,
+           adapter_ids=None):
     """y[t][o] = sum_i W_b[o][i] x[t][i] for one block.  planes: a block in
     the paged layout (repack_planes; its plane count follows from its size);
     lut: int16 [rows][2^bits] (fp16 bit patterns); x: bf16 [T][cols].
-    Returns fp32 [T][rows]."""
+    Returns fp32 [T][rows].  With adapters (the keyword arguments of
+    add_adapters: a, b and optionally scale, ranks) and adapter_ids, every
+    token's low-rank adapter is added to y in place."""
     import torch
     T, cols = x.shape
     n_max = planes.numel() * 4 // plane_bytes(rows, cols)
@@ -144,6 +155,8 @@ def linear(planes, lut, bits: int, x, rows: int, y=None, stream=None):
         y = torch.empty((T, rows), dtype=torch.float32, device=x.device)
     check(lib().pw_linear(_ptr(planes), _ptr(lut), rows, cols, n_max, bits, _ptr(x), T, _ptr(y),
                           _stream(stream)))
+    if adapters is not None:
+        add_adapters(x, ids=adapter_ids, base=y, y=y, stream=stream, **adapters)
     return y
 
 
@@ -202,6 +215,221 @@ def plan_release(blocks, target_bytes: int):
             "reached": bool(reached.value)}
 
 
+# ---- around a projection ----------------------------------------------------
+# These calls take views with a row stride, run on the tensors' device and
+# check every tensor; a refused argument raises PwError(PW_ERR_INVALID_ARG)
+# before anything is enqueued.
+
+_types = None
+
+
+def _type_codes():
+    """torch dtype -> pw_dtype_t (int16 / uint8 stand for bf16 / e4m3 bit patterns)."""
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.float32: 0, torch.bfloat16: 1, torch.int16: 1, torch.float16: 2,
+                  torch.float8_e4m3fn: 3, torch.uint8: 3}
+    return _types
+
+
+def _refuse(message: str):
+    raise PwError(1, message)
+
+
+def _rows(t, name: str, shape, device: int, types) -> int:
+    """Check a [rows][columns] tensor with contiguous rows; its row stride."""
+    if t.dim() != 2 or t.shape != shape:
+        _refuse("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.get_device() != device:
+        _refuse("%s: on another device than the other tensors" % name)
+    if _types.get(t.dtype) not in types:
+        _refuse("%s: type %s" % (name, t.dtype))
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
+        _refuse("%s: the columns of a row must be contiguous" % name)
+    return ld
+
+
+def _flat(t, name: str, shape, device: int, dtypes) -> int:
+    """Check a contiguous tensor (None passes); its address."""
+    if t is None:
+        return 0
+    if t.shape != shape:
+        _refuse("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.get_device() != device:
+        _refuse("%s: on another device than the other tensors" % name)
+    if t.dtype not in dtypes:
+        _refuse("%s: type %s" % (name, t.dtype))
+    if not t.is_contiguous():
+        _refuse("%s: must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _on_stream(fn, stream, tensors, *args, **kw):
+    """fn on `stream`, outputs allocated there and the inputs' memory kept
+    from reuse until the work on it is done."""
+    import torch
+    with torch.cuda.stream(stream):
+        out = fn(*args, **kw)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return out
+
+
+def add_rms_norm(x, weight, eps: float, residual=None, residual_out=None, y=None, scales=None,
+                 y_type=None, scale_group: int = 0, stream=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight over each row.
+
+    x [T][H] bf16 or fp32, residual [T][H] bf16 or fp32 (optional), weight
+    [H] bf16 or fp32.  y_type torch.bfloat16 (default) or torch.float8_e4m3fn;
+    the 8-bit output has fp32 scales per row (scale_group 0, [T]) or per 128
+    columns (scale_group 128, [T][ceil(H / 128)]), y ~ scale * q.
+    residual_out may be the residual itself.  Returns (y, scales or None,
+    residual_out or None)."""
+    import torch
+    if not x.is_cuda or x.dim() != 2:
+        _refuse("x: a CUDA tensor [T][H] is needed")
+    dev = x.get_device()
+    if stream is not None:
+        return _on_stream(add_rms_norm, stream, (x, weight, residual, residual_out, y, scales), x,
+                          weight, eps, residual, residual_out, y, scales, y_type, scale_group)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return add_rms_norm(x, weight, eps, residual, residual_out, y, scales, y_type,
+                                scale_group)
+    codes = _type_codes()
+    T, H = shape = x.shape
+    x_ld = _rows(x, "x", shape, dev, (0, 1))
+    w = _flat(weight, "weight", (H,), dev, (torch.bfloat16, torch.float32, torch.int16))
+    r_ld = ro_ld = r_code = 0
+    if residual is not None:
+        r_ld = _rows(residual, "residual", shape, dev, (0, 1))
+        r_code = codes[residual.dtype]
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+        ro_ld = _rows(residual_out, "residual_out", shape, dev, (r_code,))
+    elif residual_out is not None:
+        _refuse("residual_out: needs a residual")
+    if y is None:
+        y = torch.empty(shape, dtype=y_type or torch.bfloat16, device=x.device)
+    elif y_type is not None and codes.get(y.dtype) != codes.get(y_type):
+        _refuse("y: type %s, y_type %s" % (y.dtype, y_type))
+    y_ld = _rows(y, "y", shape, dev, (1, 3))
+    y_code = codes[y.dtype]
+    if y_code == 3:
+        want = (T,) if scale_group == 0 else (T, -(-H // 128))
+        if scales is None:
+            scales = torch.empty(want, dtype=torch.float32, device=x.device)
+    elif scales is not None:
+        _refuse("scales: only with an 8-bit y")
+    s = _flat(scales, "scales", want, dev, (torch.float32,)) if y_code == 3 else 0
+    status = lib().pw_add_rms_norm(x.data_ptr(), codes[x.dtype], x_ld, _ptr(residual), r_code,
+                                   r_ld, w, codes[weight.dtype], eps, T, H, _ptr(residual_out),
+                                   ro_ld, y.data_ptr(), y_code, y_ld, s, scale_group,
+                                   torch.cuda.current_stream().cuda_stream)
+    if status:
+        check(status)
+    return y, scales, residual_out
+
+
+def token_logprobs(logits, tokens=None, n_top: int = 0, logprob=None, entropy=None, top_idx=None,
+                   top_logprob=None, stream=None):
+    """Log probabilities of tokens (int32 [T], -1 for none) under a softmax
+    over each row of logits ([T][V] fp32, bf16 or fp16), the rows' entropy,
+    and the n_top best alternatives (largest first, ties to the lower index).
+    Returns (logprob fp32 [T] or None, entropy fp32 [T], top_idx int32
+    [T][n_top] or None, top_logprob fp32 [T][n_top] or None)."""
+    import torch
+    if not logits.is_cuda or logits.dim() != 2:
+        _refuse("logits: a CUDA tensor [T][V] is needed")
+    dev = logits.get_device()
+    if stream is not None:
+        return _on_stream(token_logprobs, stream,
+                          (logits, tokens, logprob, entropy, top_idx, top_logprob), logits, tokens,
+                          n_top, logprob, entropy, top_idx, top_logprob)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return token_logprobs(logits, tokens, n_top, logprob, entropy, top_idx, top_logprob)
+    codes = _type_codes()
+    T, V = shape = logits.shape
+    ld = _rows(logits, "logits", shape, dev, (0, 1, 2))
+    f32, i32 = (torch.float32,), (torch.int32,)
+
+    def out(t, name, want, dtypes):
+        if t is None:
+            t = torch.empty(want, dtype=dtypes[0], device=logits.device)
+        return t, _flat(t, name, want, dev, dtypes)
+
+    tok = lp = ti = tl = 0
+    if tokens is not None:
+        tok = _flat(tokens, "tokens", (T,), dev, i32)
+        logprob, lp = out(logprob, "logprob", (T,), f32)
+    elif logprob is not None:
+        _refuse("logprob: needs tokens")
+    entropy, ent = out(entropy, "entropy", (T,), f32)
+    if n_top > 0:
+        top_idx, ti = out(top_idx, "top_idx", (T, n_top), i32)
+        top_logprob, tl = out(top_logprob, "top_logprob", (T, n_top), f32)
+    elif top_idx is not None or top_logprob is not None:
+        _refuse("top_idx, top_logprob: need n_top > 0")
+    status = lib().pw_token_logprobs(logits.data_ptr(), codes[logits.dtype], ld, T, V, tok, n_top,
+                                     lp, ent, ti, tl, torch.cuda.current_stream().cuda_stream)
+    if status:
+        check(status)
+    return logprob, entropy, top_idx, top_logprob
+
+
+def add_adapters(x, a, b, ids, base=None, scale=None, ranks=None, y=None, y_type=None,
+                 stream=None):
+    """y[t] = base[t] + scale[i] * B_i (A_i x[t]), i = ids[t]; base[t] alone
+    where ids[t] is -1.
+
+    x bf16 [T][cols]; a bf16 [n][max_rank][cols]; b bf16 [n][rows][max_rank];
+    ids int32 [T]; scale fp32 [n] and ranks int32 [n] on the device
+    (optional); base [T][rows] fp32 or bf16 (optional; may be y); y of base's
+    type (y_type, default fp32, without a base).  Returns y."""
+    import torch
+    if not x.is_cuda or x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        _refuse("CUDA tensors x [T][cols], a [n][max_rank][cols], b [n][rows][max_rank] are needed")
+    dev = x.get_device()
+    if stream is not None:
+        return _on_stream(add_adapters, stream, (x, a, b, ids, base, scale, ranks, y), x, a, b, ids,
+                          base, scale, ranks, y, y_type)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return add_adapters(x, a, b, ids, base, scale, ranks, y, y_type)
+    codes = _type_codes()
+    T, cols = x.shape
+    n, rows, r = b.shape
+    bf16 = (torch.bfloat16, torch.int16)
+    if ids is None:
+        _refuse("ids: an adapter index for each token is needed")
+    x_ld = _rows(x, "x", x.shape, dev, (1,))
+    pa = _flat(a, "a", (n, r, cols), dev, bf16)
+    pb = _flat(b, "b", b.shape, dev, bf16)
+    pi = _flat(ids, "ids", (T,), dev, (torch.int32,))
+    pr = _flat(ranks, "ranks", (n,), dev, (torch.int32,))
+    ps = _flat(scale, "scale", (n,), dev, (torch.float32,))
+    shape, base_ld, pbase = (T, rows), 0, 0
+    if base is not None:
+        base_ld = _rows(base, "base", shape, dev, (0, 1))
+        pbase = base.data_ptr()
+    if y is None:
+        dtype = base.dtype if base is not None else y_type or torch.float32
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+    y_ld = _rows(y, "y", shape, dev, (0, 1) if base is None else (codes[base.dtype],))
+    if y_type is not None and codes.get(y_type) != codes[y.dtype]:
+        _refuse("y: type %s, y_type %s" % (y.dtype, y_type))
+    status = lib().pw_adapters(x.data_ptr(), x_ld, pa, pb, pi, pr, ps, n, r, T, cols, rows, pbase,
+                               base_ld, y.data_ptr(), codes[y.dtype], y_ld,
+                               torch.cuda.current_stream().cuda_stream)
+    if status:
+        check(status)
+    return y
+
+
 class MoELayer:
     """A layer over device-resident pages (torch tensors kept alive here)."""
 
@@ -236,6 +464,21 @@ class MoELayer:
         check(lib().pw_moe_forward(self.h, _ptr(x), T, _ptr(router_w), _ptr(bias), _ptr(y),
                                    _stream(stream)))
         return y
+
+    def forward_norm(self, x, norm_weight, eps: float, router_w, bias=None, residual=None,
+                     residual_out=None, y=None, stream=None):
+        """forward of x' = add_rms_norm(x, norm_weight, eps, residual): all
+        bf16 and contiguous.  Returns (y, residual_out or None)."""
+        import torch
+        T = x.shape[0]
+        if y is None:
+            y = torch.empty_like(x)
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(residual)
+        check(lib().pw_moe_forward_norm(self.h, _ptr(x), _ptr(residual), _ptr(norm_weight), eps, T,
+                                        _ptr(router_w), _ptr(bias), _ptr(residual_out), _ptr(y),
+                                        _stream(stream)))
+        return y, residual_out
 
     def forward_host(self, x_host, router_w, bias=None, y_host=None, stream=None):
         """x_host: pinned CPU int16/bf16 tensor [T][H]; returns the host output."""

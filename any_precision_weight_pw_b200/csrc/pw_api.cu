@@ -948,6 +948,28 @@ pw_status_t pw_moe_forward_host(pw_moe_t* h, const uint16_t* x_host, int32_t T,
   return PW_OK;
 }
 
+pw_status_t pw_moe_forward_norm(pw_moe_t* h, const uint16_t* d_x, const uint16_t* d_residual,
+                                const uint16_t* d_norm_w, float eps, int32_t T,
+                                const float* d_router_w, const float* d_router_bias,
+                                uint16_t* d_residual_out, uint16_t* d_y, pw_stream_t stream) {
+  if (!h) return fail(PW_ERR_INVALID_ARG, "null handle");
+  if (T < 0 || T > h->cfg.max_tokens)
+    return fail(PW_ERR_INVALID_ARG, "T = %d outside [0, max_tokens = %d]", T, h->cfg.max_tokens);
+  if (T > 0 && (!d_x || !d_norm_w || !d_router_w || !d_y))
+    return fail(PW_ERR_INVALID_ARG, "null buffer");
+  if (!aligned16(d_x) || !aligned16(d_residual) || !aligned16(d_norm_w) ||
+      !aligned16(d_residual_out) || !aligned16(d_router_w) || !aligned16(d_y))
+    return fail(PW_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
+  // the norm's output takes the place pw_moe_forward_host copies its rows to
+  const int32_t H = h->cfg.hidden;
+  const pw_status_t st = pw_add_rms_norm(d_x, PW_BF16, H, d_residual, PW_BF16, H, d_norm_w, PW_BF16,
+                                         eps, T, H, d_residual_out, H, h->stage_x, PW_BF16, H,
+                                         nullptr, 0, stream);
+  if (st != PW_OK) return st;
+  return forward_impl(h, h->stage_x, T, d_router_w, d_router_bias, d_y,
+                      static_cast<cudaStream_t>(stream));
+}
+
 pw_status_t pw_linear(const uint32_t* d_planes, const uint16_t* d_lut, int32_t rows, int32_t cols,
                       int32_t n_max, int32_t bits, const uint16_t* d_x, int32_t T, float* d_y,
                       pw_stream_t stream) {

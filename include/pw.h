@@ -383,6 +383,91 @@ pw_status_t pw_route_static(const uint16_t* d_x, const float* d_router_w,
                             int32_t n_experts, int32_t top_k, int32_t renorm_topk,
                             int32_t* d_idx, float* d_w, pw_stream_t stream);
 
+/* ---- around a projection ------------------------------------------------ */
+
+/* Element types of the calls below. */
+typedef enum { PW_F32 = 0, PW_BF16 = 1, PW_F16 = 2, PW_E4M3 = 3 } pw_dtype_t;
+
+/* Residual addition and root-mean-square norm, the step before a projection
+ * or an MoE layer:
+ *   h = x + residual (fp32; residual NULL: h = x), residual_out = round(h),
+ *   y = h * (mean(h^2) + eps)^-1/2 * weight.
+ * d_x [T][H] and d_residual [T][H] PW_BF16 or PW_F32, d_weight [H] PW_BF16 or
+ * PW_F32, d_residual_out [T][H] of the residual's type (NULL: not written).
+ * The norm takes the unrounded h.  y_type PW_BF16: d_y bf16, d_scales unused.
+ * y_type PW_E4M3: d_y holds q = e4m3(y / s) with s = max(max|y| / 448, 2^-126)
+ * over the row (scale_group 0, d_scales fp32 [T]) or over each 128 columns of
+ * it (scale_group 128, d_scales fp32 [T][ceil(H / 128)]); y ~ s * q, and a row
+ * (group) holding NaN has s = NaN.
+ *   Strides count elements between rows (inputs: 0 repeats one row); rows are
+ * contiguous.  Buffers need only their elements' alignment; 16-byte aligned
+ * rows with H a multiple of 8 are read in 16-byte pieces.  d_residual_out may
+ * be d_residual, d_y may be d_x (same type and stride); other overlaps are
+ * undefined.  T >= 0 (0: nothing is done), 1 <= H <= 32768
+ * (PW_ERR_UNSUPPORTED above), eps > 0. */
+pw_status_t pw_add_rms_norm(const void* d_x, int32_t x_type, int64_t x_stride,
+                            const void* d_residual, int32_t residual_type,
+                            int64_t residual_stride, const void* d_weight, int32_t weight_type,
+                            float eps, int32_t T, int32_t H, void* d_residual_out,
+                            int64_t residual_out_stride, void* d_y, int32_t y_type,
+                            int64_t y_stride, float* d_scales, int32_t scale_group,
+                            pw_stream_t stream);
+
+/* Log probabilities of given tokens under a softmax over each row of logits,
+ * with the rows' entropy and their n_top best alternatives: for logits z,
+ * m = max z, S = sum exp(z - m),
+ *   log p_j = z_j - m - ln S,  entropy = ln S - sum p_j (z_j - m),
+ *   top: the n_top largest logits, largest first, ties to the lower index
+ *   (+0 and -0 are equal, NaN ranks above all).
+ * d_logits [T][V] of PW_F32, PW_BF16 or PW_F16 with stride elements between
+ * rows (contiguous rows; only the elements' alignment is needed); d_tokens
+ * int32 [T] or NULL; d_logprob fp32 [T] (NULL exactly if d_tokens is);
+ * d_entropy fp32 [T] or NULL; d_top_idx int32 and d_top_logprob fp32
+ * [T][n_top] (NULL if n_top is 0).  0 <= n_top <= min(V, PW_MAX_TOP_LOGPROBS).
+ *   Token -1 stands for none: its log probability is written as 0.  A token
+ * outside [-1, V) gives NaN.  Masked logits are -inf: log p = -inf, nothing
+ * added to the entropy.  A row with every logit -inf has log p = -inf
+ * throughout and entropy 0.  A row holding +inf or NaN has NaN log
+ * probabilities and entropy (-inf logits keep -inf).  T >= 0, V >= 1. */
+#define PW_MAX_TOP_LOGPROBS 32
+pw_status_t pw_token_logprobs(const void* d_logits, int32_t logits_type, int64_t stride, int32_t T,
+                              int32_t V, const int32_t* d_tokens, int32_t n_top,
+                              float* d_logprob, float* d_entropy, int32_t* d_top_idx,
+                              float* d_top_logprob, pw_stream_t stream);
+
+/* Low-rank adapters of many requests beside one shared projection
+ * (pw_linear): for token t with adapter a = d_ids[t],
+ *   y_t = base_t + scale_a * B_a (A_a x_t),
+ * and y_t = base_t where a is -1 (any a outside [0, n_adapters) counts as -1).
+ * d_x bf16 [T][cols]; d_a bf16 [n_adapters][max_rank][cols]; d_b bf16
+ * [n_adapters][rows][max_rank]; d_ids int32 [T], in any order; d_ranks int32
+ * [n_adapters] or NULL (all max_rank): rows of A_a and columns of B_a from
+ * rank_a on are not used (values are taken into [0, max_rank]); d_scale fp32
+ * [n_adapters] or NULL (all 1); d_base [T][rows] and d_y [T][rows] of y_type
+ * PW_F32 or PW_BF16; d_base may be NULL (0) or d_y (same stride).  x and y
+ * strides count elements between rows; rows, A and B are contiguous.  Buffers
+ * need only their elements' alignment; 16-byte aligned rows are read in
+ * 16-byte pieces.  Accumulation is fp32, A_a x_t enters the second product
+ * with 24 (y fp32) or 16 (y bf16) significant bits.  T >= 0,
+ * 1 <= max_rank <= PW_MAX_ADAPTER_RANK.  One launch, no workspace. */
+#define PW_MAX_ADAPTER_RANK 256
+#define PW_MAX_ADAPTERS 4194303
+pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const uint16_t* d_a,
+                        const uint16_t* d_b, const int32_t* d_ids, const int32_t* d_ranks,
+                        const float* d_scale, int32_t n_adapters, int32_t max_rank, int32_t T,
+                        int32_t cols, int32_t rows, const void* d_base, int64_t base_stride,
+                        void* d_y, int32_t y_type, int64_t y_stride, pw_stream_t stream);
+
+/* pw_moe_forward of a pre-norm block: y = MoE(x') with x' the bf16 y of
+ * pw_add_rms_norm(x, residual, norm_w, eps); residual_out as there.  d_x bf16
+ * [T][H], d_residual bf16 [T][H] or NULL, d_norm_w bf16 [H], d_residual_out
+ * bf16 [T][H] or NULL (may be d_residual), all contiguous and 16-byte
+ * aligned.  x' is kept in the handle's workspace.  d_y may be d_x. */
+pw_status_t pw_moe_forward_norm(pw_moe_t* h, const uint16_t* d_x, const uint16_t* d_residual,
+                                const uint16_t* d_norm_w, float eps, int32_t T,
+                                const float* d_router_w, const float* d_router_bias,
+                                uint16_t* d_residual_out, uint16_t* d_y, pw_stream_t stream);
+
 const char* pw_last_error(void);
 int32_t pw_abi_version(void);
 
