@@ -26,7 +26,7 @@ EXPORTED = ["pw_moe_create", "pw_set_block_bits", "pw_moe_forward", "pw_destroy"
             "pw_get_forward_bits", "pw_set_switch_lag", "pw_routing_stats", "pw_plan_release",
             "pw_enable_paging", "pw_resident_bytes", "pw_workspace_bytes", "pw_compact_pages",
             "pw_last_error", "pw_abi_version", "pw_route_geometry", "pw_add_rms_norm",
-            "pw_token_logprobs", "pw_adapters", "pw_moe_forward_norm"]
+            "pw_token_logprobs", "pw_adapters", "pw_adapters_workspace_bytes", "pw_moe_forward_norm"]
 
 
 class PwError(RuntimeError):
@@ -97,13 +97,15 @@ def lib():
                                       i64, P, i32, i64, P, i32, P]
         L.pw_token_logprobs.argtypes = [P, i32, i64, i32, i32, P, i32, P, P, P, P, P]
         L.pw_adapters.argtypes = [P, i64, P, P, P, P, P, i32, i32, i32, i32, i32, P, i64, P, i32,
-                                  i64, P]
+                                  i64, P, i64, P]
+        L.pw_adapters_workspace_bytes.argtypes = [i32, i32, i32]
+        L.pw_adapters_workspace_bytes.restype = i64
         L.pw_moe_forward_norm.argtypes = [P, P, P, P, C.c_float, i32, P, P, P, P, P]
         L.pw_last_error.restype = C.c_char_p
         L.pw_abi_version.restype = i32
         for name in EXPORTED:
             if name not in ("pw_forward_launches", "pw_last_error", "pw_abi_version",
-                            "pw_plane_bytes"):
+                            "pw_plane_bytes", "pw_adapters_workspace_bytes"):
                 getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
@@ -284,7 +286,7 @@ def add_rms_norm(x, weight, eps: float, residual=None, residual_out=None, y=None
 
     x [T][H] bf16 or fp32, residual [T][H] bf16 or fp32 (optional), weight
     [H] bf16 or fp32.  y_type torch.bfloat16 (default) or torch.float8_e4m3fn;
-    the 8-bit output has fp32 scales per row (scale_group 0, [T]) or per 128
+    the 8-bit output has fp32 scales per row (scale_group 0, [T][1]) or per 128
     columns (scale_group 128, [T][ceil(H / 128)]), y ~ scale * q.
     residual_out may be the residual itself.  Returns (y, scales or None,
     residual_out or None)."""
@@ -319,7 +321,7 @@ def add_rms_norm(x, weight, eps: float, residual=None, residual_out=None, y=None
     y_ld = _rows(y, "y", shape, dev, (1, 3))
     y_code = codes[y.dtype]
     if y_code == 3:
-        want = (T,) if scale_group == 0 else (T, -(-H // 128))
+        want = (T, 1 if scale_group == 0 else -(-H // 128))
         if scales is None:
             scales = torch.empty(want, dtype=torch.float32, device=x.device)
     elif scales is not None:
@@ -422,8 +424,12 @@ def add_adapters(x, a, b, ids, base=None, scale=None, ranks=None, y=None, y_type
     y_ld = _rows(y, "y", shape, dev, (0, 1) if base is None else (codes[base.dtype],))
     if y_type is not None and codes.get(y_type) != codes[y.dtype]:
         _refuse("y: type %s, y_type %s" % (y.dtype, y_type))
+    work, size = 0, lib().pw_adapters_workspace_bytes(T, r, codes[y.dtype])
+    if size:
+        keep = torch.empty(size, dtype=torch.uint8, device=x.device)
+        work = keep.data_ptr()
     status = lib().pw_adapters(x.data_ptr(), x_ld, pa, pb, pi, pr, ps, n, r, T, cols, rows, pbase,
-                               base_ld, y.data_ptr(), codes[y.dtype], y_ld,
+                               base_ld, y.data_ptr(), codes[y.dtype], y_ld, work, size,
                                torch.cuda.current_stream().cuda_stream)
     if status:
         check(status)

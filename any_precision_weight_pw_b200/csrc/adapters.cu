@@ -1,24 +1,27 @@
 // adapters.cu -- pw_adapters: low-rank adapters of many requests beside one
 // shared projection, y_t = base_t + scale_a * B_a (A_a x_t), a = ids[t].
 //
-// One launch, no workspace.  A cluster of 8 blocks takes R tokens and keeps
-// everything between its two products on chip:
-//   order    the tokens of a window of 256 are taken in the order of their
-//            adapters where they are mixed, so tokens that share an adapter
-//            meet in one cluster, and cut into pieces of at most 16 tokens of
-//            one adapter (the rows of an MMA tile);
-//   shrink   v = A_a x: block c of the cluster takes an eighth of the columns,
-//            its warps split that again; the partial sums meet over distributed
-//            shared memory, in a fixed order;
-//   expand   y = base + B_a (scale v): block c takes an eighth of the rows.
 // Both products run on mma.sync m16n8k16 (bf16, fp32 accumulation) straight
 // from global memory: the contraction index may be permuted freely as long as
-// both operands agree, so each lane loads 16 (shrink) or 8 (expand) contiguous
-// bytes of a row and uses them as its fragments of two or one MMA steps.
-// At ranks up to 64 the operator needs at most about 50 operations a byte, a
-// fifth of what this GPU's tensor cores could do per byte of its memory, so
-// the wide tcgen05 tiles, which would need x and B staged in shared memory,
-// have nothing to win here; what counts is bytes in flight.
+// both operands agree, so each lane loads 16 (shrink, v = A x) or 8 (expand,
+// y += B v) contiguous bytes of a row and uses them as its fragments of two or
+// one MMA steps.  At ranks up to 64 the operator needs at most about 50
+// operations a byte, a fifth of what this GPU's tensor cores could do per byte
+// of its memory, so the wide tcgen05 tiles, which would need x, B and base
+// staged in shared memory, have nothing to win here; what counts is bytes in
+// flight and the length of the chain of dependent loads.
+//
+// The tokens of a window of 256 are taken in the order of their adapters, and
+// cut into pieces of at most 16 tokens of one adapter (the rows of an MMA
+// tile): tokens that share an adapter share its reads.
+//   Few tokens (at most kNarrow): one launch, a cluster of 8 blocks per piece,
+//     each an eighth of the columns, then of the rows; v's partial sums meet
+//     over distributed shared memory.  What the second product reads besides v
+//     is loaded before the barrier.
+//   Many tokens: shrink_kernel, clusters of 8 over 64 ordered tokens, leaves v
+//     and the pieces in the workspace; expand_kernel walks (64 tokens) x (512
+//     rows) tiles, all equal work, next base tile in flight.
+// Every sum has a fixed order: results do not depend on timing.
 //
 // Precision.  v is split into bf16 terms (v = hi + mid + lo, 24 bits; two
 // terms, 16 bits, when y is bf16 and rounds to 8), each multiplied with B
@@ -27,6 +30,7 @@
 
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "pw_internal.h"
 
@@ -36,8 +40,9 @@ namespace {
 constexpr int kAdThreads = 256;
 constexpr int kAdWarps = kAdThreads / 32;
 constexpr int kAdCluster = 8;
-constexpr int kWindow = 256;   // tokens ordered together
-constexpr int kMaxRows = 64;   // tokens of a cluster
+constexpr int kWindow = 256;     // tokens ordered together
+constexpr int kNarrow = 512;     // most tokens of the one-launch path
+constexpr int kTileTokens = 64;  // many tokens: tokens of a cluster / tile
 constexpr int kMaxDevices = 64;
 
 struct AdapterParams {
@@ -49,14 +54,14 @@ struct AdapterParams {
   const float* scale;
   const void* base;
   void* y;
+  uint8_t* ws;
   int64_t x_ld, base_ld, y_ld;
   int n, r_max, T, cols, rows;
-  int R;          // tokens of a cluster (a power of two, at most 16 * MT)
-  int v_ld;       // bf16 elements between the rows of v in shared memory
-  int vec_x;      // 16-byte loads of x and A are legal
-  int vec_b;      // 8-byte loads of B are legal
-  int vec_y;      // 16-byte (fp32) or 8-byte (bf16) accesses of base and y are legal
-  int y_f32;
+  int per_window;  // clusters of a full window (few tokens)
+  int v_ld;        // bf16 elements between the rows of v
+  int n_terms;     // bf16 terms of v
+  int tile_rows;   // many tokens: rows of an expand tile
+  int r32;         // max_rank in whole 32s
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -93,24 +98,50 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// `count` (at most 8) bf16 from p on, zero past them, as 16 bytes
-__device__ __forceinline__ uint4 load8(const uint16_t* p, int count, bool vec) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (count <= 0) return v;
-  if (vec) return __ldg(reinterpret_cast<const uint4*>(p));
+// 8 bf16 from column c of a row of `cols`, zero past the row; VEC: the row and
+// c are 16-byte aligned, cols % 8 == 0
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int cols) {
+  const uint16_t* p = row + c;
+  const int count = cols - c;
+  if (count <= 0) return make_uint4(0, 0, 0, 0);
+  if constexpr (VEC) return __ldg(reinterpret_cast<const uint4*>(p));
+  if (c >= 3 && count >= 12) {
+    // inside the row at any alignment: the three aligned 8-byte words around
+    // the 16 bytes, shifted by whole and half words
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 7;
+    const uint2* w = reinterpret_cast<const uint2*>(reinterpret_cast<uintptr_t>(p) - off);
+    const uint2 w0 = __ldg(w), w1 = __ldg(w + 1), w2 = __ldg(w + 2);
+    const bool one = off & 4;
+    const uint32_t a = one ? w0.y : w0.x, b = one ? w1.x : w0.y, d = one ? w1.y : w1.x,
+                   e = one ? w2.x : w1.y, f = one ? w2.y : w2.x;
+    const uint32_t s = (off & 2) * 8;
+    return make_uint4(__funnelshift_r(a, b, s), __funnelshift_r(b, d, s), __funnelshift_r(d, e, s),
+                      __funnelshift_r(e, f, s));
+  }
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = i < count ? __ldg(p + i) : 0u;
   return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
 }
-__device__ __forceinline__ uint2 load4(const uint16_t* p, int count, bool vec) {
-  uint2 v = make_uint2(0, 0);
-  if (count <= 0) return v;
-  if (vec && count >= 4) return __ldg(reinterpret_cast<const uint2*>(p));
-  uint32_t w[4];
+// the first `count` of 4 bf16, zero past them; VEC: 8-byte aligned, and a whole
+// row of B follows a multiple of 4 ranks
+template <bool VEC>
+__device__ __forceinline__ uint2 load4(const uint16_t* p, int count) {
+  if (count <= 0) return make_uint2(0, 0);
+  if constexpr (VEC) {
+    uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    if (count < 4) {
+      v.y &= count == 3 ? 0xffffu : 0u;
+      v.x &= count == 1 ? 0xffffu : 0xffffffffu;
+    }
+    return v;
+  } else {
+    uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = i < count ? __ldg(p + i) : 0u;
-  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    for (int i = 0; i < 4; ++i) w[i] = i < count ? __ldg(p + i) : 0u;
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+  }
 }
 
 __device__ __forceinline__ float bf16_value(uint16_t b) {
@@ -124,82 +155,454 @@ struct Piece {
   int start, len, adapter, rank;  // rank 0: nothing to add (no adapter)
 };
 
-// MT: pieces worked on at once (the warps split into MT groups); NT: 8-wide
-// rank tiles of a shrink step (rank chunks of 8 * NT).
-template <int MT, int NT>
-__global__ void __launch_bounds__(kAdThreads) adapter_kernel(const AdapterParams p) {
-  constexpr int KW = kAdWarps / MT;       // warps sharing a piece
-  constexpr int kChunk = 8 * NT;          // ranks of a shrink step
-  constexpr int kTile = 16 * kChunk;      // partial sums of a piece and step
-  constexpr bool kTwoStep = MT > 1;       // partial sums: reduce-scatter + all-gather
-  // slots: one step, every block gets every block's sums (two buffers in turn);
-  // two steps, a block gets its eighth of them
-  constexpr int kSlot = kTwoStep ? MT * kTile / kAdCluster : kTile;
-  extern __shared__ __align__(16) uint8_t smem[];
-  float* red = reinterpret_cast<float*>(smem);             // [8 warps][16][kChunk]
-  float* slots = red + kAdWarps * kTile;                   // [2 or 1][8 blocks][kSlot]
-  uint16_t* vt = reinterpret_cast<uint16_t*>(slots + (kTwoStep ? 1 : 2) * kAdCluster * kSlot);
-  __shared__ __align__(16) int s_key[kWindow];
-  __shared__ int s_tok[kMaxRows], s_id[kMaxRows];
-  __shared__ Piece s_piece[kMaxRows];
-  __shared__ int s_np;
-
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const int rank = static_cast<int>(cluster_rank());
-  const int cl = blockIdx.x / kAdCluster;
-  const int per_window = kWindow / p.R;
-  const int t0 = cl / per_window * kWindow;               // the window's first token
-  const int n_win = min(kWindow, p.T - t0);
-  const int first = cl % per_window * p.R;                // the cluster's first position
-  const int n_rows = min(p.R, n_win - first);             // >= 1 by the grid
-  cluster_arrive();  // the other blocks' shared memory is live once all have arrived
-  pdl_wait();
-
-  // ---- order: this cluster's tokens and its pieces ------------------------
-  if (p.R == 1) {
-    if (tid == 0) {
-      const int id = p.ids[t0 + first];
-      s_tok[0] = t0 + first;
-      s_id[0] = id >= 0 && id < p.n ? id : -1;
-    }
-  } else {
-    int id = -1;
-    if (tid < n_win) {
-      id = p.ids[t0 + tid];
-      if (id < 0 || id >= p.n) id = -1;
-    }
-    // id 0..n-1, none = 2^22 - 1; the position in the low 8 bits
-    const int key = ((id < 0 ? PW_MAX_ADAPTERS : id) << 8) | tid;
-    s_key[tid] = tid < n_win ? key : INT32_MAX;
-    __syncthreads();
-    const bool change = tid > 0 && tid < n_win && (s_key[tid - 1] >> 8) != (key >> 8);
-    const int runs = 1 + __syncthreads_count(change);
-    int pos = tid;
-    if (runs * 16 > n_win) {  // mixed: position = number of smaller keys
-      pos = 0;
-      for (int i = 0; i < n_win; i += 4) {
-        const int4 k4 = *reinterpret_cast<const int4*>(s_key + i);
-        pos += (k4.x < key) + (k4.y < key) + (k4.z < key) + (k4.w < key);
-      }
-    }
-    if (tid < n_win && pos >= first && pos < first + n_rows) {
-      s_tok[pos - first] = t0 + tid;
-      s_id[pos - first] = id;
+// Window order in shared memory: position -> token of the window and adapter
+// (-1 for none, behind the others).  All 256 threads; key: scratch.  Windows
+// whose runs are long as they are stay so if keep_runs.
+__device__ __forceinline__ void order_window(const AdapterParams& p, int t0, int n_win,
+                                             bool keep_runs, int* key, int* tok, int* sid) {
+  const int tid = threadIdx.x;
+  int id = -1;
+  if (tid < n_win) {
+    id = p.ids[t0 + tid];
+    if (id < 0 || id >= p.n) id = -1;
+  }
+  // no adapter: 2^22 - 1, above every other; the position in the low 8 bits
+  const int k = ((id < 0 ? PW_MAX_ADAPTERS : id) << 8) | tid;
+  key[tid] = tid < n_win ? k : INT32_MAX;
+  __syncthreads();
+  const bool change = tid > 0 && tid < n_win && (key[tid - 1] >> 8) != (k >> 8);
+  const int runs = 1 + __syncthreads_count(change);
+  int pos = tid;
+  if (keep_runs ? runs * 16 > n_win : runs > 1) {  // position = number of smaller keys
+    pos = 0;
+    for (int i = 0; i < n_win; i += 4) {
+      const int4 k4 = *reinterpret_cast<const int4*>(key + i);
+      pos += (k4.x < k) + (k4.y < k) + (k4.z < k) + (k4.w < k);
     }
   }
+  if (tid < n_win) {
+    tok[pos] = t0 + tid;
+    sid[pos] = id;
+  }
   __syncthreads();
+}
+
+__device__ __forceinline__ int adapter_rank(const AdapterParams& p, int id) {
+  if (id < 0) return 0;
+  return p.ranks ? min(max(p.ranks[id], 0), p.r_max) : p.r_max;
+}
+
+// ---- the two products --------------------------------------------------------
+
+// Partial sums of a piece's v for ranks [r0, r0 + 8 NT) over the 32-column
+// blocks kb0, kb0 + step, ... < kb1.  tok: the piece's tokens.
+template <bool VEC, int NT>
+__device__ __forceinline__ void shrink_acc(const AdapterParams& p, const Piece& pc, const int* tok,
+                                           int r0, int kb0, int kb1, int step, float (&acc)[NT][4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int nr = pc.rank - r0;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+  if (nr <= 0) return;
+  const int c0 = g < pc.len ? p.cols : 0, c1 = g + 8 < pc.len ? p.cols : 0;  // columns there are
+  const uint16_t* x0 = p.x + (c0 ? tok[g] : 0) * p.x_ld;
+  const uint16_t* x1 = p.x + (c1 ? tok[g + 8] : 0) * p.x_ld;
+  const uint16_t* ar = p.a + (static_cast<int64_t>(pc.adapter) * p.r_max + r0 + g) * p.cols;
+#pragma unroll (NT == 8 ? 1 : 2)
+  for (int kb = kb0; kb < kb1; kb += step) {
+    const int c = kb * 32 + q * 8;
+    const uint4 xa = load8<VEC>(x0, c, c0);
+    const uint4 xb = load8<VEC>(x1, c, c1);
+    uint4 w[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      w[j] = load8<VEC>(ar + static_cast<int64_t>(8 * j) * p.cols, c, 8 * j + g < nr ? p.cols : 0);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      mma16816(acc[j], xa.x, xb.x, xa.y, xb.y, w[j].x, w[j].y);
+      mma16816(acc[j], xa.z, xb.z, xa.w, xb.w, w[j].z, w[j].w);
+    }
+  }
+}
+
+// acc of a warp to its [16][8 NT] tile in shared memory
+template <int NT>
+__device__ __forceinline__ void store_acc(float* tile, const float (&acc)[NT][4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    *reinterpret_cast<float2*>(tile + g * 8 * NT + 8 * j + 2 * q) = make_float2(acc[j][0], acc[j][1]);
+    *reinterpret_cast<float2*>(tile + (g + 8) * 8 * NT + 8 * j + 2 * q) =
+        make_float2(acc[j][2], acc[j][3]);
+  }
+}
+
+// The next bf16 term of two neighbouring values, as one word.  Infinities and
+// NaN are whole in the first.
+__device__ __forceinline__ uint32_t next_term(float (&v)[2]) {
+  uint16_t h[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    h[i] = bf16_bits(v[i]);
+    const float hv = bf16_value(h[i]);
+    v[i] = fabsf(hv) < INFINITY ? v[i] - hv : 0.f;
+  }
+  return h[0] | static_cast<uint32_t>(h[1]) << 16;
+}
+
+// 16 tokens x 16 rows of the second product.  MMA column g of tile j is row
+// o + 4 (g / 2) + 2 j + g % 2: a lane then holds rows 4q..4q+3, whole 16-byte
+// accesses of base and y.
+// F32: type of base and y.  VEC: every access is aligned and rows % 4 == 0.
+template <int KS, bool F32, bool VEC>
+struct ExpandTile {
+  static constexpr int kTerms = F32 ? 3 : 2;
+  using E = typename std::conditional<F32, float, uint16_t>::type;
+  using Raw4 = typename std::conditional<F32, float4, uint2>::type;
+
+  // A lane's tokens (rows g and g + 8 of the piece) and its place in B and v.
+  struct Lane {
+    const E* base[2];
+    E* y[2];
+    const uint16_t* b;
+    const uint16_t* v;
+    bool on[2], any_base;
+    __device__ __forceinline__ Lane(const AdapterParams& p, const Piece& pc, const int* tok,
+                                    const uint16_t* v_rows) {
+      const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        on[h] = g + 8 * h < pc.len;
+        const int64_t t = on[h] ? tok[g + 8 * h] : 0;
+        base[h] = static_cast<const E*>(p.base) + t * p.base_ld + 4 * q;
+        y[h] = static_cast<E*>(p.y) + t * p.y_ld + 4 * q;
+      }
+      any_base = p.base != nullptr;
+      b = p.b + (static_cast<int64_t>(max(pc.adapter, 0)) * p.rows + 4 * (g >> 1) + (g & 1)) * p.r_max +
+          4 * q;
+      v = v_rows + g * p.v_ld + 4 * q;
+    }
+  };
+
+  Raw4 add[2];     // [token half]: base as it lies in memory
+  uint2 w[KS][2];  // B, a 16-rank step each
+
+  // base, and B of ranks [0, 16 KS)
+  __device__ __forceinline__ void load(const AdapterParams& p, const Piece& pc, const Lane& l, int ob) {
+    const int left = p.rows - ob * 16 - 4 * static_cast<int>(threadIdx.x & 3);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const E* src = l.base[h] + ob * 16;
+      Raw4 r = {};
+      if (l.any_base && l.on[h] && left > 0) {
+        if constexpr (VEC) {
+          r = *reinterpret_cast<const Raw4*>(src);
+        } else {
+          E e[4] = {src[0], left > 1 ? src[1] : E(0), left > 2 ? src[2] : E(0),
+                    left > 3 ? src[3] : E(0)};
+          if constexpr (F32)
+            r = make_float4(e[0], e[1], e[2], e[3]);
+          else
+            r = make_uint2(e[0] | static_cast<uint32_t>(e[1]) << 16,
+                           e[2] | static_cast<uint32_t>(e[3]) << 16);
+        }
+      }
+      add[h] = r;
+    }
+    load_b(p, pc, l, ob, 0);
+  }
+  __device__ __forceinline__ void load_b(const AdapterParams& p, const Piece& pc, const Lane& l,
+                                         int ob, int k0) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int ro = ob * 16 + 4 * (g >> 1) + (g & 1), count = pc.rank - k0 - 4 * q;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint16_t* src = l.b + static_cast<int64_t>(ob * 16 + 2 * j) * p.r_max + k0;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        w[ks][j] = load4<VEC>(src + 16 * ks, ro + 2 * j < p.rows ? count - 16 * ks : 0);
+    }
+  }
+  // left: ranks from k0 on
+  __device__ __forceinline__ void multiply(const AdapterParams& p, const Lane& l, int v_plane, int k0,
+                                           int left, float (&acc)[2][4]) const {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      if (16 * ks >= left) break;
+#pragma unroll
+      for (int t = 0; t < kTerms; ++t) {
+        const uint16_t* vp = l.v + t * v_plane + k0 + 16 * ks;
+        const uint2 lo = *reinterpret_cast<const uint2*>(vp);
+        const uint2 hi = *reinterpret_cast<const uint2*>(vp + 8 * p.v_ld);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mma16816(acc[j], lo.x, hi.x, lo.y, hi.y, w[ks][j].x, w[ks][j].y);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(const AdapterParams& p, const Lane& l, int ob,
+                                        const float (&acc)[2][4]) const {
+    const int left = p.rows - ob * 16 - 4 * static_cast<int>(threadIdx.x & 3);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!l.on[h] || left <= 0) continue;
+      const Raw4 r = add[h];
+      float v[4];
+      if constexpr (F32) {
+        v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+      } else {
+        v[0] = __uint_as_float(r.x << 16), v[1] = __uint_as_float(r.x & 0xffff0000u);
+        v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xffff0000u);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += acc[i >> 1][2 * h + (i & 1)];
+      E* dst = l.y[h] + ob * 16;
+      if constexpr (VEC) {
+        if constexpr (F32)
+          *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(bf16_bits(v[0]) | static_cast<uint32_t>(bf16_bits(v[1])) << 16,
+                         bf16_bits(v[2]) | static_cast<uint32_t>(bf16_bits(v[3])) << 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < left) {
+            if constexpr (F32)
+              dst[i] = v[i];
+            else
+              dst[i] = bf16_bits(v[i]);
+          }
+      }
+    }
+  }
+};
+
+// The second product of one piece over 16-row blocks ob, ob + step, ... < ob1,
+// D tiles in flight.  Ranks above 16 KS take further steps (MULTI).
+template <int D, bool MULTI, int KS, bool F32, bool VEC>
+struct Expand {
+  using Tile = ExpandTile<KS, F32, VEC>;
+  Tile t[D];
+  __device__ __forceinline__ void start(const AdapterParams& p, const Piece& pc,
+                                        const typename Tile::Lane& l, int ob, int ob1, int step) {
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (ob + d * step < ob1) t[d].load(p, pc, l, ob + d * step);
+  }
+  __device__ __forceinline__ void run(const AdapterParams& p, const Piece& pc,
+                                      const typename Tile::Lane& l, int v_plane, int ob, int ob1,
+                                      int step) {
+    while (ob < ob1) {
+#pragma unroll
+      for (int d = 0; d < D; ++d, ob += step) {
+        if (ob >= ob1) return;
+        float acc[2][4] = {};
+        t[d].multiply(p, l, v_plane, 0, pc.rank, acc);
+        if (MULTI)
+          for (int k0 = 16 * KS; k0 < pc.rank; k0 += 16 * KS) {
+            t[d].load_b(p, pc, l, ob, k0);
+            t[d].multiply(p, l, v_plane, k0, pc.rank - k0, acc);
+          }
+        t[d].store(p, l, ob, acc);
+        if (ob + D * step < ob1) t[d].load(p, pc, l, ob + D * step);
+      }
+    }
+  }
+};
+
+// ---- few tokens: one launch, a cluster per piece -----------------------------
+
+template <int NT, bool MULTI, bool F32, bool VEC>
+__global__ void __launch_bounds__(kAdThreads, 2) adapter_kernel(const AdapterParams p) {
+  constexpr int kChunk = 8 * NT;       // ranks of a shrink step
+  constexpr int kTile = 16 * kChunk;   // sums of a piece and step
+  constexpr int KS = NT / 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* red = reinterpret_cast<float*>(smem);  // [8 warps][16][kChunk]
+  float* slots = red + kAdWarps * kTile;        // [1, MULTI 2][8 blocks][16][kChunk]
+  uint16_t* vt = reinterpret_cast<uint16_t*>(slots + (MULTI ? 2 : 1) * kAdCluster * kTile);
+  __shared__ __align__(16) int s_key[kWindow];
+  __shared__ int s_tok[kWindow], s_sid[kWindow];
+  __shared__ uint32_t s_mask[2][kAdWarps];
+  __shared__ Piece s_piece;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_rank());
+  const int cl = blockIdx.x / kAdCluster;
+  const int t0 = cl / p.per_window * kWindow;  // the window's first token
+  const int n_win = min(kWindow, p.T - t0);
+  const int want = cl % p.per_window;          // this cluster's piece
+  pdl_wait();
+
+  if (p.T == 1) {
+    if (tid == 0) {
+      const int id = p.ids[0], a = id >= 0 && id < p.n ? id : -1;
+      s_tok[0] = 0;
+      s_piece = {0, 1, a, adapter_rank(p, a)};
+    }
+    __syncthreads();
+  } else {
+    order_window(p, t0, n_win, false, s_key, s_tok, s_sid);
+    if (tid == 0) s_piece = {0, 0, -1, 0};
+    // a piece starts where the adapter changes and at every 16th token of a run
+    const bool change = tid < n_win && (tid == 0 || s_sid[tid] != s_sid[tid - 1]);
+    const uint32_t cm = __ballot_sync(0xffffffffu, change);
+    if (lane == 0) s_mask[0][warp] = cm;
+    __syncthreads();
+    int run = 0;
+    for (int w = warp; w >= 0; --w) {
+      const uint32_t m = s_mask[0][w] & (w == warp ? 0xffffffffu >> (31 - lane) : 0xffffffffu);
+      if (m) {
+        run = w * 32 + 31 - __clz(m);
+        break;
+      }
+    }
+    const bool start = tid < n_win && (tid - run) % 16 == 0;
+    const uint32_t sm = __ballot_sync(0xffffffffu, start);
+    if (lane == 0) s_mask[1][warp] = sm;
+    __syncthreads();
+    if (start) {
+      int index = __popc(sm & ((1u << lane) - 1));
+      for (int w = 0; w < warp; ++w) index += __popc(s_mask[1][w]);
+      if (index == want) {
+        int end = n_win;
+        for (int w = warp; w < kAdWarps; ++w) {
+          const uint32_t m = s_mask[1][w] & (w > warp    ? 0xffffffffu
+                                             : lane == 31 ? 0u
+                                                          : 0xffffffffu << (lane + 1));
+          if (m) {
+            end = w * 32 + __ffs(m) - 1;
+            break;
+          }
+        }
+        s_piece = {tid, end - tid, s_sid[tid], adapter_rank(p, s_sid[tid])};
+      }
+    }
+    __syncthreads();
+  }
+  const Piece pc = s_piece;  // the same in all blocks of the cluster
+  if (pc.len == 0 || (pc.rank == 0 && p.base == p.y)) return;
+  const int* tok = s_tok + pc.start;
+  if (pc.rank > 0) cluster_arrive();  // the others' shared memory is live once all have arrived
+
+  // this block's columns (shrink, in 32s) and rows (expand, in 16s)
+  const int kb_all = (p.cols + 31) / 32, ob_all = (p.rows + 15) / 16;
+  const int kb0 = rank * kb_all / kAdCluster, kb1 = (rank + 1) * kb_all / kAdCluster;
+  const int ob0 = rank * ob_all / kAdCluster + warp, ob1 = (rank + 1) * ob_all / kAdCluster;
+  const int v_plane = 16 * p.v_ld;
+  const float sc = pc.adapter >= 0 && p.scale ? p.scale[pc.adapter] : 1.f;
+
+  using Tile = ExpandTile<KS, F32, VEC>;
+  const typename Tile::Lane l(p, pc, tok, vt);
+  Expand<MULTI ? 1 : KS == 4 ? 2 : 4, MULTI, KS, F32, VEC> second;
+  if (pc.rank == 0) second.start(p, pc, l, ob0, ob1, kAdWarps);
+  auto shrink = [&](int r0, int step) {
+    float acc[NT][4];
+    shrink_acc<VEC, NT>(p, pc, tok, r0, kb0 + warp, kb1, kAdWarps, acc);
+    store_acc<NT>(red + warp * kTile, acc);
+    if (r0 == 0) {
+      second.start(p, pc, l, ob0, ob1, kAdWarps);  // in flight over the exchange
+      cluster_wait();
+    }
+    __syncthreads();
+    // this block's sums to every block, rows in use only
+    float* slot = slots + (MULTI ? (step & 1) * kAdCluster * kTile : 0);
+    for (int e = tid * 4; e < pc.len * kChunk; e += kAdThreads * 4) {
+      float4 s = *reinterpret_cast<const float4*>(red + e);
+#pragma unroll
+      for (int k = 1; k < kAdWarps; ++k) {
+        const float4 o = *reinterpret_cast<const float4*>(red + k * kTile + e);
+        s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+      }
+      const uint32_t d = smem_u32(slot + rank * kTile + e);
+#pragma unroll
+      for (int c = 0; c < kAdCluster; ++c) put4(in_block(d, c), s);
+    }
+    cluster_arrive();
+    cluster_wait();
+    // sums over the blocks; scale v and split it into bf16 terms
+    for (int e = tid * 2; e < kTile; e += kAdThreads * 2) {
+      const int row = e / kChunk, k = r0 + e % kChunk;
+      if (k >= p.v_ld) continue;
+      float v[2] = {0.f, 0.f};
+      if (row < pc.len) {
+#pragma unroll
+        for (int c = 0; c < kAdCluster; ++c) {
+          const float2 o = *reinterpret_cast<const float2*>(slot + c * kTile + e);
+          v[0] += o.x, v[1] += o.y;
+        }
+        v[0] *= sc, v[1] *= sc;
+      }
+#pragma unroll
+      for (int t = 0; t < Tile::kTerms; ++t)
+        *reinterpret_cast<uint32_t*>(vt + t * v_plane + row * p.v_ld + k) = next_term(v);
+    }
+    __syncthreads();
+  };
+  if (pc.rank > 0) {
+    shrink(0, 0);
+    if constexpr (MULTI)
+      for (int r0 = kChunk, step = 1; r0 < pc.rank; r0 += kChunk, ++step) shrink(r0, step);
+  }
+  second.run(p, pc, l, v_plane, ob0, ob1, kAdWarps);
+}
+
+// ---- many tokens: shrink, then expand ----------------------------------------
+
+// What shrink leaves for expand, per 64 tokens: the segments (neighbours of
+// one adapter), the tokens, and v (n_terms planes of [64][v_ld] bf16, by
+// position, zero from the rank on to the next multiple of 32).
+struct TileInfo {
+  int n_segments, pad[3];
+  Piece segment[kTileTokens];
+  int tok[kTileTokens];
+};
+__host__ __device__ __forceinline__ int64_t tile_bytes(int n_terms, int v_ld) {
+  return static_cast<int64_t>(sizeof(TileInfo)) + 2ll * n_terms * kTileTokens * v_ld;
+}
+
+template <int NT, bool VEC>
+__global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterParams p) {
+  constexpr int MT = 4;                // pieces at once, two warps each
+  constexpr int KW = kAdWarps / MT;
+  constexpr int kChunk = 8 * NT;
+  constexpr int kTile = 16 * kChunk;
+  constexpr int kSlot = MT * kTile / kAdCluster;  // sums a block owns
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* red = reinterpret_cast<float*>(smem);  // [8 warps][16][kChunk]
+  float* slots = red + kAdWarps * kTile;        // [8 blocks][kSlot]
+  __shared__ __align__(16) int s_key[kWindow];
+  __shared__ int s_tok[kWindow], s_sid[kWindow];
+  __shared__ Piece s_piece[kTileTokens];
+  __shared__ int s_np;
+  __shared__ uint64_t s_changes;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_rank());
+  const int cl = blockIdx.x / kAdCluster;
+  constexpr int kPerWindow = kWindow / kTileTokens;
+  const int t0 = cl / kPerWindow * kWindow;
+  const int n_win = min(kWindow, p.T - t0);
+  const int first = cl % kPerWindow * kTileTokens;
+  const int n_rows = min(kTileTokens, n_win - first);  // >= 1 by the grid
+  cluster_arrive();  // the others' shared memory is live once all have arrived
+  pdl_wait();
+  pdl_trigger();  // expand's blocks may start; they wait for this grid's end
+  order_window(p, t0, n_win, true, s_key, s_tok, s_sid);
+  const int* tok = s_tok + first;
+  const int* sid = s_sid + first;
   if (warp == 0) {
     // a piece starts where the adapter changes and at every 16th token of a run
-    uint64_t changes = 0;
+    uint64_t changes = 0, starts = 0;
+    bool is_start[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int i = lane + 32 * half;
-      const bool c = i < n_rows && (i == 0 || s_id[i] != s_id[i - 1]);
+      const bool c = i < n_rows && (i == 0 || sid[i] != sid[i - 1]);
       changes |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, c)) << (32 * half);
     }
-    uint64_t starts = 0;
-    bool is_start[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int i = lane + 32 * half;
@@ -212,73 +615,50 @@ __global__ void __launch_bounds__(kAdThreads) adapter_kernel(const AdapterParams
       const int i = lane + 32 * half;
       if (!is_start[half]) continue;
       const uint64_t above = i == 63 ? 0ull : starts & (~0ull << (i + 1));
-      const int id = s_id[i];
-      int r = 0;
-      if (id >= 0) r = p.ranks ? min(max(p.ranks[id], 0), p.r_max) : p.r_max;
       s_piece[__popcll(starts & ((1ull << i) - 1))] = {
-          i, (above ? __ffsll(above) - 1 : n_rows) - i, id, r};
+          i, (above ? __ffsll(above) - 1 : n_rows) - i, sid[i], adapter_rank(p, sid[i])};
     }
-    if (lane == 0) s_np = __popcll(starts);
+    if (lane == 0) {
+      s_np = __popcll(starts);
+      s_changes = changes;
+    }
   }
   __syncthreads();
   const int n_pieces = s_np;
-  const int mp = warp % MT, kw = warp / MT;  // piece and share of this warp
-
-  // this block's columns (shrink, in 32s) and rows (expand, in 32s)
-  const int kb_all = (p.cols + 31) / 32, ob_all = (p.rows + 31) / 32;
+  uint8_t* ws = p.ws + cl * tile_bytes(p.n_terms, p.v_ld);
+  if (rank == 0) {
+    TileInfo* info = reinterpret_cast<TileInfo*>(ws);
+    if (tid < n_rows) info->tok[tid] = tok[tid];
+    if (warp == 0) {
+      const uint64_t changes = s_changes;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int i = lane + 32 * half;
+        if (!(changes >> i & 1)) continue;
+        const uint64_t above = i == 63 ? 0ull : changes & (~0ull << (i + 1));
+        info->segment[__popcll(changes & ((1ull << i) - 1))] = {
+            i, (above ? __ffsll(above) - 1 : n_rows) - i, sid[i], adapter_rank(p, sid[i])};
+      }
+      if (lane == 0) info->n_segments = __popcll(changes);
+    }
+  }
+  uint16_t* vt = reinterpret_cast<uint16_t*>(ws + sizeof(TileInfo));
+  const int v_plane = kTileTokens * p.v_ld;
+  const int mp = warp % MT, kw = warp / MT;
+  const int kb_all = (p.cols + 31) / 32;
   const int kb0 = rank * kb_all / kAdCluster, kb1 = (rank + 1) * kb_all / kAdCluster;
-  const int ob0 = rank * ob_all / kAdCluster, ob1 = (rank + 1) * ob_all / kAdCluster;
-  const int v_plane = 16 * MT * p.v_ld;      // one bf16 term of v
-  const int n_terms = p.y_f32 ? 3 : 2;
   cluster_wait();
-
-  int step = 0;  // exchange steps done: the one-step slots alternate
   for (int p0 = 0; p0 < n_pieces; p0 += MT) {
     Piece pc = {0, 0, -1, 0};
     if (p0 + mp < n_pieces) pc = s_piece[p0 + mp];
     int r_all = 0;  // largest rank of this pass: the same in all blocks
     for (int i = p0; i < min(n_pieces, p0 + MT); ++i) r_all = max(r_all, s_piece[i].rank);
-
-    // ---- shrink ------------------------------------------------------------
-    for (int r0 = 0; r0 < r_all; r0 += kChunk, ++step) {
+    for (int r0 = 0; r0 < r_all; r0 += kChunk) {
       float acc[NT][4];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-      const int nr = min(kChunk, pc.rank - r0);  // ranks of this piece here (may be <= 0)
-      if (nr > 0) {
-        const uint16_t* x0 = p.x + (g < pc.len ? s_tok[pc.start + g] : 0) * p.x_ld;
-        const uint16_t* x1 = p.x + (g + 8 < pc.len ? s_tok[pc.start + g + 8] : 0) * p.x_ld;
-        const uint16_t* ar = p.a + (static_cast<int64_t>(pc.adapter) * p.r_max + r0 + g) * p.cols;
-#pragma unroll 2
-        for (int kb = kb0 + kw; kb < kb1; kb += KW) {
-          const int c = kb * 32 + q * 8;
-          const int left = p.cols - c;
-          const uint4 xa = load8(x0 + c, g < pc.len ? left : 0, p.vec_x);
-          const uint4 xb = load8(x1 + c, g + 8 < pc.len ? left : 0, p.vec_x);
-          uint4 w[NT];
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            w[j] = load8(ar + static_cast<int64_t>(8 * j) * p.cols + c, 8 * j + g < nr ? left : 0,
-                         p.vec_x);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            mma16816(acc[j], xa.x, xb.x, xa.y, xb.y, w[j].x, w[j].y);
-            mma16816(acc[j], xa.z, xb.z, xa.w, xb.w, w[j].z, w[j].w);
-          }
-        }
-      }
-      float* mine = red + warp * kTile;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        *reinterpret_cast<float2*>(mine + g * kChunk + 8 * j + 2 * q) =
-            make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2*>(mine + (g + 8) * kChunk + 8 * j + 2 * q) =
-            make_float2(acc[j][2], acc[j][3]);
-      }
+      shrink_acc<VEC, NT>(p, pc, tok + pc.start, r0, kb0 + kw, kb1, KW, acc);
+      store_acc<NT>(red + warp * kTile, acc);
       __syncthreads();
-      // sums over this block's warps, to the blocks that need them
+      // each block's sums to the block that owns them
       for (int e = tid * 4; e < MT * kTile; e += kAdThreads * 4) {
         const int m = e / kTile, i = e % kTile;
         float4 s = *reinterpret_cast<const float4*>(red + m * kTile + i);
@@ -287,193 +667,309 @@ __global__ void __launch_bounds__(kAdThreads) adapter_kernel(const AdapterParams
           const float4 o = *reinterpret_cast<const float4*>(red + (k * MT + m) * kTile + i);
           s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
         }
-        if (kTwoStep) {
-          put4(in_block(smem_u32(slots + rank * kSlot + e % kSlot), e / kSlot), s);
-        } else {
-          const uint32_t d = smem_u32(slots + ((step & 1) * kAdCluster + rank) * kSlot + e);
-#pragma unroll
-          for (int c = 0; c < kAdCluster; ++c) put4(in_block(d, c), s);
-        }
+        put4(in_block(smem_u32(slots + rank * kSlot + e % kSlot), e / kSlot), s);
       }
       cluster_arrive();
       cluster_wait();
-      // sums over the blocks; scale v and split it into bf16 terms
-      const float* from = slots + (kTwoStep ? 0 : (step & 1) * kAdCluster * kSlot);
       for (int e = tid * 2; e < kSlot; e += kAdThreads * 2) {
-        float2 s = make_float2(0.f, 0.f);
+        const int f = rank * kSlot + e;  // of [MT][16][kChunk]
+        const int m = f / kTile, row = f % kTile / kChunk, k = r0 + f % kChunk;
+        if (k >= p.r32 || p0 + m >= n_pieces) continue;
+        const Piece& o = s_piece[p0 + m];
+        if (row >= o.len || o.rank == 0) continue;
+        const float sc = p.scale ? p.scale[o.adapter] : 1.f;
+        float v[2] = {0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < kAdCluster; ++c) {
-          const float2 o = *reinterpret_cast<const float2*>(from + c * kSlot + e);
-          s.x += o.x, s.y += o.y;
+          const float2 w = *reinterpret_cast<const float2*>(slots + c * kSlot + e);
+          v[0] += w.x, v[1] += w.y;
         }
-        const int f = kTwoStep ? rank * kSlot + e : e;  // [MT][16][kChunk]
-        const int m = f / kTile, row = f % kTile / kChunk, k = r0 + f % kChunk;
-        if (k >= p.v_ld || p0 + m >= n_pieces) continue;
-        const int id = s_piece[p0 + m].adapter;
-        const float sc = id >= 0 && p.scale ? p.scale[id] : 1.f;
-        float v[2] = {s.x * sc, s.y * sc};
-        const uint32_t d = smem_u32(vt + (m * 16 + row) * p.v_ld + k);
-        for (int t = 0; t < n_terms; ++t) {
-          uint16_t h[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            h[i] = bf16_bits(v[i]);
-            const float hv = bf16_value(h[i]);
-            v[i] = fabsf(hv) < INFINITY ? v[i] - hv : 0.f;  // infinities and NaN are whole in one term
-          }
-          const uint32_t w = h[0] | static_cast<uint32_t>(h[1]) << 16;
-          if (kTwoStep) {
-#pragma unroll
-            for (int c = 0; c < kAdCluster; ++c)
-              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                               in_block(d + static_cast<uint32_t>(t * v_plane * 2), c)),
-                           "r"(w)
-                           : "memory");
-          } else {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(d + static_cast<uint32_t>(t * v_plane * 2)),
-                         "r"(w)
-                         : "memory");
-          }
+        v[0] *= sc, v[1] *= sc;
+        for (int t = 0; t < p.n_terms; ++t) {
+          uint16_t* d = vt + t * v_plane + (o.start + row) * p.v_ld + k;
+          *reinterpret_cast<uint32_t*>(d) = next_term(v);
+          if (kChunk == 16) *reinterpret_cast<uint32_t*>(d + 16) = 0;
         }
       }
-      if (kTwoStep) {
-        cluster_arrive();
-        cluster_wait();
-      } else {
-        __syncthreads();
-      }
-    }
-
-    // ---- expand --------------------------------------------------------------
-    if (pc.len > 0 && (pc.rank > 0 || p.base != p.y)) {
-      const bool on0 = g < pc.len, on1 = g + 8 < pc.len;
-      const int64_t row0 = on0 ? s_tok[pc.start + g] : 0, row1 = on1 ? s_tok[pc.start + g + 8] : 0;
-      const uint16_t* vrow = vt + (mp * 16 + g) * p.v_ld + 4 * q;
-      const uint16_t* br = p.b + static_cast<int64_t>(pc.adapter) * p.rows * p.r_max;
-      // n index g of MMA tile j is row o + 16 (j / 2) + 4 (g / 2) + 2 (j % 2) + g % 2:
-      // a lane then holds rows 4q..4q+3 of each half of the 32
-      const int og = 4 * (g >> 1) + (g & 1);
-      for (int ob = ob0 + kw; ob < ob1; ob += KW) {
-        const int o = ob * 32;
-        float acc[4][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-        float add[2][2][4];  // [token half][row half]: base
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int c = o + 16 * w + 4 * q;
-            const int64_t at = (h ? row1 : row0) * p.base_ld + c;
-            float* d = add[h][w];
-            d[0] = d[1] = d[2] = d[3] = 0.f;
-            if (!p.base || !(h ? on1 : on0) || c >= p.rows) continue;
-            if (p.y_f32) {
-              const float* src = static_cast<const float*>(p.base) + at;
-              if (p.vec_y) {
-                const float4 v = *reinterpret_cast<const float4*>(src);
-                d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (c + i < p.rows) d[i] = src[i];
-              }
-            } else {
-              const uint16_t* src = static_cast<const uint16_t*>(p.base) + at;
-              if (p.vec_y) {
-                const uint2 v = *reinterpret_cast<const uint2*>(src);
-                d[0] = __uint_as_float(v.x << 16), d[1] = __uint_as_float(v.x & 0xffff0000u);
-                d[2] = __uint_as_float(v.y << 16), d[3] = __uint_as_float(v.y & 0xffff0000u);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (c + i < p.rows) d[i] = bf16_value(src[i]);
-              }
-            }
-          }
-#pragma unroll 2
-        for (int k0 = 0; k0 < pc.rank; k0 += 16) {
-          uint2 w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int ro = o + 16 * (j >> 1) + 2 * (j & 1) + og;
-            w[j] = load4(br + static_cast<int64_t>(ro) * p.r_max + k0 + 4 * q,
-                         ro < p.rows ? pc.rank - k0 - 4 * q : 0, p.vec_b);
-          }
-          for (int t = 0; t < n_terms; ++t) {
-            const uint16_t* vp = vrow + t * v_plane + k0;
-            const uint2 lo = *reinterpret_cast<const uint2*>(vp);
-            const uint2 hi = *reinterpret_cast<const uint2*>(vp + 8 * p.v_ld);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma16816(acc[j], lo.x, hi.x, lo.y, hi.y, w[j].x, w[j].y);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int c = o + 16 * w + 4 * q;
-            if (!(h ? on1 : on0) || c >= p.rows) continue;
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = add[h][w][i] + acc[2 * w + (i >> 1)][2 * h + (i & 1)];
-            const int64_t at = (h ? row1 : row0) * p.y_ld + c;
-            if (p.y_f32) {
-              float* dst = static_cast<float*>(p.y) + at;
-              if (p.vec_y) {
-                *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (c + i < p.rows) dst[i] = v[i];
-              }
-            } else {
-              uint16_t* dst = static_cast<uint16_t*>(p.y) + at;
-              if (p.vec_y) {
-                *reinterpret_cast<uint2*>(dst) =
-                    make_uint2(bf16_bits(v[0]) | static_cast<uint32_t>(bf16_bits(v[1])) << 16,
-                               bf16_bits(v[2]) | static_cast<uint32_t>(bf16_bits(v[3])) << 16);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (c + i < p.rows) dst[i] = bf16_bits(v[i]);
-              }
-            }
-          }
-      }
+      // the sums have been read before the next step's arrive
+      cluster_arrive();
+      cluster_wait();
     }
   }
 }
 
-template <int MT, int NT>
-cudaError_t launch_shape(const AdapterParams& p, cudaStream_t s) {
-  constexpr int kTile = 16 * 8 * NT;
-  constexpr size_t kSums =
-      sizeof(float) * (kAdWarps * kTile + (MT > 1 ? MT * kTile : 2 * kAdCluster * kTile));
-  constexpr int kMaxLd = PW_MAX_ADAPTER_RANK + 16;
-  const size_t smem = kSums + sizeof(uint16_t) * (p.y_f32 ? 3 : 2) * 16 * MT * p.v_ld;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+constexpr int kBlk = 64;  // rows (of W) of an expand step
+
+// y = base + B v over (64 tokens) x (tile_rows rows) tiles.  Per step (one
+// segment of the tile, 64 rows) base [64][64] and B [64][rank] are copied to
+// shared memory asynchronously, STAGES - 1 steps ahead.  Warp w multiplies
+// tokens 16 (w % 4) .. + 15 with rows 32 (w / 4) .. + 31.  Within both operands
+// a lane holds 8 consecutive ranks of each 32 (two MMA steps).  Shared-memory
+// rows are a multiple of 128 bytes or 64 apart; 16-byte pieces are swapped by
+// row so that 8 lanes of two (base fp32, B) or four (base bf16) rows take all
+// banks.
+// KS: 32-rank steps, v's fragments stay in registers; 0: any number, from
+// shared memory.
+template <int KS, bool F32, bool VEC, int STAGES>
+__global__ void __launch_bounds__(kAdThreads, KS ? 2 : 1) expand_kernel(const AdapterParams p) {
+  constexpr int kTerms = F32 ? 3 : 2;
+  constexpr int kES = F32 ? 4 : 2;  // bytes of an element of y
+  constexpr int kRow = kBlk * kES, kPieces = kRow / 16;
+  constexpr int kRowsAt = kAdThreads / kPieces;  // tile rows a pass of the block copies
+  constexpr int kPasses = kTileTokens / kRowsAt;
+  constexpr int kBase = kTileTokens * kRow;      // bytes of a stage's base
+  using E = typename std::conditional<F32, float, uint16_t>::type;
+  extern __shared__ __align__(16) uint8_t smem[];  // stages
+  __shared__ TileInfo s_info;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3, mp = warp & 3, half = warp >> 2;
+  const int v_plane = kTileTokens * p.v_ld;
+  const int r32 = KS ? 32 * KS : p.r32;
+  const int b_row = 2 * r32, b_pieces = r32 / 8;  // bytes, 16-byte pieces of a row of B
+  const int b_swap = b_row % 128 == 0 ? 4 : 0;
+  const int stage_bytes = kBase + kBlk * b_row;
+  const int n_chunks = (p.rows + p.tile_rows - 1) / p.tile_rows;
+  const int64_t tile = blockIdx.x / n_chunks;
+  const int first = blockIdx.x % n_chunks * p.tile_rows;  // the block's rows
+  const int rows = min(p.rows - first, p.tile_rows), nb = (rows + kBlk - 1) / kBlk;
+  const E* base = static_cast<const E*>(p.base);
+  const bool in_place = p.base == p.y;
+  const uint8_t* ws = p.ws + tile * tile_bytes(kTerms, p.v_ld);
+  const uint16_t* vt = reinterpret_cast<const uint16_t*>(ws + sizeof(TileInfo));
+  pdl_wait();
+  if (tid < static_cast<int>(sizeof(TileInfo) / 16))
+    reinterpret_cast<uint4*>(&s_info)[tid] = reinterpret_cast<const uint4*>(ws)[tid];
+  __syncthreads();
+  const int n_segments = s_info.n_segments;
+
+  // The copies run ahead, with their own place.  A thread copies one 16-byte
+  // piece of every kRowsAt-th row of base and of every few rows of B.
+  int l_seg = 0, l_blk = 0, l_stage = 0;
+  Piece l_sg;
+  const E* l_base[kPasses];
+  const uint16_t* l_b = nullptr;
+  int l_bytes = 0;  // of the thread's piece of B, inside the rank
+  const int row_a = tid / kPieces, pc_a = tid % kPieces;
+  const int row_b = tid / b_pieces, pc_b = tid % b_pieces;
+  const int b_step = kAdThreads / b_pieces;  // rows a pass copies (b_pieces divides 256 if KS)
+  const uint32_t dst_a = smem_u32(smem) + row_a * kRow +
+                         (F32 ? pc_a ^ (row_a & 1) << 2 : pc_a ^ (row_a & 3) << 1) * 16;
+  const uint32_t dst_b = smem_u32(smem) + kBase + row_b * b_row + (pc_b ^ (row_b & 1) * b_swap) * 16;
+  auto open_segment = [&]() {
+    l_sg = s_info.segment[l_seg];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = min(row_a + i * kRowsAt, l_sg.len - 1);
+      l_base[i] = base + s_info.tok[l_sg.start + r] * p.base_ld + first + pc_a * (16 / kES);
+    }
+    l_b = p.b + (static_cast<int64_t>(max(l_sg.adapter, 0)) * p.rows + first) * p.r_max;
+    l_bytes = min(max(2 * (l_sg.rank - 8 * pc_b), 0), 16);
+    if (VEC && KS) l_b += static_cast<int64_t>(row_b) * p.r_max + pc_b * 8;
+  };
+  auto issue = [&]() {
+    if (l_seg < n_segments) {
+      if (l_blk == 0) open_segment();
+      const int left = rows - l_blk * kBlk;  // rows of W from this step on
+      const uint32_t at = l_stage * stage_bytes;
+      if (l_sg.rank > 0 || !in_place) {
+        if (p.base) {
+          if constexpr (VEC) {
+            const int bytes = pc_a * (16 / kES) < left ? 16 : 0;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i)
+              if (row_a + i * kRowsAt < l_sg.len)
+                cp_async16(dst_a + at + i * kRowsAt * kRow, bytes ? l_base[i] + l_blk * kBlk : base,
+                           bytes);
+          } else {
+#pragma unroll 4
+            for (int i = tid; i < l_sg.len * kBlk; i += kAdThreads) {
+              const int row = i / kBlk, c = i % kBlk, pc = c * kES / 16;
+              const int sw = F32 ? pc ^ (row & 1) << 2 : pc ^ (row & 3) << 1;
+              E v = E(0);
+              if (c < left)
+                v = (base + s_info.tok[l_sg.start + row] * p.base_ld)[first + l_blk * kBlk + c];
+              *reinterpret_cast<E*>(smem + at + row * kRow + sw * 16 + c * kES % 16) = v;
+            }
+          }
+        }
+        const uint16_t* b = l_b + static_cast<int64_t>(l_blk * kBlk) * p.r_max;
+        if constexpr (VEC && KS) {
+#pragma unroll
+          for (int i = 0; i < kBlk * 4 * KS / kAdThreads; ++i) {
+            const int bytes = row_b + i * b_step < left ? l_bytes : 0;
+            cp_async16(dst_b + at + i * b_step * b_row, bytes ? b + i * b_step * p.r_max : p.b, bytes);
+          }
+        } else if constexpr (VEC) {
+          for (int i = tid; i < kBlk * b_pieces; i += kAdThreads) {
+            const int row = i / b_pieces, pc = i % b_pieces;
+            const int bytes = row < left ? min(max(2 * (l_sg.rank - 8 * pc), 0), 16) : 0;
+            cp_async16(smem_u32(smem) + at + kBase + row * b_row + (pc ^ (row & 1) * b_swap) * 16,
+                       bytes ? b + static_cast<int64_t>(row) * p.r_max + pc * 8 : p.b, bytes);
+          }
+        } else {
+#pragma unroll 4
+          for (int i = tid; i < kBlk * r32; i += kAdThreads) {
+            const int row = i / r32, k = i % r32;
+            uint16_t v = 0;
+            if (k < l_sg.rank && row < left) v = b[static_cast<int64_t>(row) * p.r_max + k];
+            *reinterpret_cast<uint16_t*>(smem + at + kBase + row * b_row +
+                                         (k / 8 ^ (row & 1) * b_swap) * 16 + k % 8 * 2) = v;
+          }
+        }
+      }
+      l_stage = l_stage + 1 == STAGES ? 0 : l_stage + 1;
+      if (++l_blk == nb) l_blk = 0, ++l_seg;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) issue();
+
+  // this lane's places within a stage
+  const int m0 = mp * 16, col = half * 32 + 4 * q;
+  const uint8_t* at_b = smem + kBase + (half * 32 + 4 * (g >> 1) + (g & 1)) * b_row;
+  const uint8_t* at_base[2];  // row m0 + g, row halves; row m0 + g + 8 is 8 kRow behind
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int at = (col + 16 * w) * kES, pc = at / 16;
+    at_base[w] = smem + (m0 + g) * kRow + (F32 ? pc ^ (g & 1) << 2 : pc ^ (g & 3) << 1) * 16 + at % 16;
+  }
+  int stage = 0;
+  for (int seg = 0; seg < n_segments; ++seg) {
+    const Piece sg = s_info.segment[seg];
+    const int n_k = (sg.rank + 31) / 32;
+    const bool work = m0 < sg.len && (sg.rank > 0 || !in_place);
+    // rows behind the segment's last stand for nothing and are not stored
+    const uint16_t* v0 = vt + min(sg.start + m0 + g, kTileTokens - 1) * p.v_ld + 8 * q;
+    const uint16_t* v1 = vt + min(sg.start + m0 + g + 8, kTileTokens - 1) * p.v_ld + 8 * q;
+    uint4 vf[KS ? KS : 1][kTerms][2];  // v's fragments of the segment
+    if (KS && work) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        if (k < n_k)
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) {
+            vf[k][t][0] = *reinterpret_cast<const uint4*>(v0 + t * v_plane + 32 * k);
+            vf[k][t][1] = *reinterpret_cast<const uint4*>(v1 + t * v_plane + 32 * k);
+          }
+    }
+    E* y[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      y[h] = static_cast<E*>(p.y) +
+             s_info.tok[min(sg.start + m0 + g + 8 * h, sg.start + sg.len - 1)] * p.y_ld + first + col;
+    for (int blk = 0; blk < nb; ++blk) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+      __syncthreads();  // this step's data is there; the last step's has been read
+      issue();
+      const int at = stage * stage_bytes;
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      if (!work) continue;
+      // MMA column g of tile j is row 16 (j / 2) + 4 (g / 2) + 2 (j % 2) + g % 2
+      const uint8_t* bp = at_b + at;
+      float acc[4][4] = {};
+      auto step = [&](int k, const uint4(&f)[kTerms][2]) {
+        const int pc = (4 * k + q) ^ (g & 1) * b_swap;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 w =
+              *reinterpret_cast<const uint4*>(bp + (16 * (j >> 1) + 2 * (j & 1)) * b_row + pc * 16);
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) {
+            mma16816(acc[j], f[t][0].x, f[t][1].x, f[t][0].y, f[t][1].y, w.x, w.y);
+            mma16816(acc[j], f[t][0].z, f[t][1].z, f[t][0].w, f[t][1].w, w.z, w.w);
+          }
+        }
+      };
+      if constexpr (KS > 0) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          if (k < n_k) step(k, vf[k]);
+      } else {
+        for (int k = 0; k < n_k; ++k) {
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) {
+            vf[0][t][0] = *reinterpret_cast<const uint4*>(v0 + t * v_plane + 32 * k);
+            vf[0][t][1] = *reinterpret_cast<const uint4*>(v1 + t * v_plane + 32 * k);
+          }
+          step(k, vf[0]);
+        }
+      }
+      const int left = rows - blk * kBlk - col;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (m0 + g + 8 * h >= sg.len) continue;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (left <= 16 * w) continue;
+          float v[4] = {};
+          if (p.base) {
+            const uint8_t* src = at_base[w] + at + 8 * h * kRow;
+            if constexpr (F32) {
+              const float4 b = *reinterpret_cast<const float4*>(src);
+              v[0] = b.x, v[1] = b.y, v[2] = b.z, v[3] = b.w;
+            } else {
+              const uint2 b = *reinterpret_cast<const uint2*>(src);
+              v[0] = __uint_as_float(b.x << 16), v[1] = __uint_as_float(b.x & 0xffff0000u);
+              v[2] = __uint_as_float(b.y << 16), v[3] = __uint_as_float(b.y & 0xffff0000u);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] += acc[2 * w + (i >> 1)][2 * h + (i & 1)];
+          E* dst = y[h] + blk * kBlk + 16 * w;
+          if constexpr (VEC) {
+            if constexpr (F32)
+              *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+            else
+              *reinterpret_cast<uint2*>(dst) =
+                  make_uint2(bf16_bits(v[0]) | static_cast<uint32_t>(bf16_bits(v[1])) << 16,
+                             bf16_bits(v[2]) | static_cast<uint32_t>(bf16_bits(v[3])) << 16);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i < left - 16 * w) {
+                if constexpr (F32)
+                  dst[i] = v[i];
+                else
+                  dst[i] = bf16_bits(v[i]);
+              }
+          }
+        }
+      }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// ---- host ------------------------------------------------------------------
+
+// The kernel's dynamic shared memory limit, once per device.
+template <auto kernel>
+cudaError_t allow_smem(size_t bytes) {
   static std::mutex mu;
-  static bool attr_set[kMaxDevices] = {};
+  static size_t allowed[kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!attr_set[dev]) {
-      e = cudaFuncSetAttribute(adapter_kernel<MT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(kSums + sizeof(uint16_t) * 3 * 16 * MT * kMaxLd));
-      if (e != cudaSuccess) return e;
-      attr_set[dev] = true;
-    }
-  }
-  const int per_window = kWindow / p.R;
-  const int full = p.T / kWindow, rest = p.T % kWindow;
-  const int64_t clusters = static_cast<int64_t>(full) * per_window + (rest + p.R - 1) / p.R;
+  std::lock_guard<std::mutex> lock(mu);
+  if (allowed[dev] >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+  if (e == cudaSuccess) allowed[dev] = bytes;
+  return e;
+}
+
+template <typename K>
+cudaError_t launch(K* kernel, int64_t grid, int cluster, size_t smem, cudaStream_t s,
+                   const AdapterParams& p) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kAdCluster));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kAdThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -481,19 +977,74 @@ cudaError_t launch_shape(const AdapterParams& p, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kAdCluster;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, adapter_kernel<MT, NT>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int MT>
-cudaError_t launch_rank(const AdapterParams& p, cudaStream_t s) {
-  if (p.r_max <= 16) return launch_shape<MT, 2>(p, s);
-  if (p.r_max <= 32) return launch_shape<MT, 4>(p, s);
-  return launch_shape<MT, 8>(p, s);
+// v's rows in shared memory, in elements.  Few tokens: whole 16-rank steps, 32
+// or 96 bytes modulo 128 apart, so that the four rows of half a warp's 8-byte
+// loads take all banks.  Many: whole 32s, 64 modulo 128 bytes apart, two rows
+// of 16-byte loads.
+int v_stride(int max_rank) {
+  const int r16 = (max_rank + 15) / 16 * 16;
+  return r16 % 32 == 0 ? r16 + 16 : r16;
+}
+int wide_v_stride(int max_rank) {
+  const int r32 = (max_rank + 31) / 32 * 32;
+  return r32 % 64 == 0 ? r32 + 32 : r32;
+}
+
+template <int NT, bool MULTI, bool F32, bool VEC>
+cudaError_t launch_shape(AdapterParams p, int n_sm, cudaStream_t s) {
+  constexpr int kTile = 16 * 8 * NT;
+  cudaError_t e;
+  if (p.T <= kNarrow) {
+    // a window holds at most one piece per 16 tokens and one more per adapter
+    // or none at all
+    const int64_t most = static_cast<int64_t>(p.n) + 1 + kWindow / 16;
+    p.per_window = static_cast<int>(most < kWindow ? most : kWindow);
+    const int full = p.T / kWindow, rest = p.T % kWindow;
+    const int64_t last = static_cast<int64_t>(p.n) + 1 + rest / 16;
+    const int64_t clusters = static_cast<int64_t>(full) * p.per_window +
+                             (last < rest ? last : rest);
+    const size_t smem = sizeof(float) * kTile * (kAdWarps + (MULTI ? 2 : 1) * kAdCluster) +
+                        sizeof(uint16_t) * p.n_terms * 16 * p.v_ld;
+    e = allow_smem<adapter_kernel<NT, MULTI, F32, VEC>>(smem);
+    if (e != cudaSuccess) return e;
+    return launch(adapter_kernel<NT, MULTI, F32, VEC>, clusters * kAdCluster, kAdCluster, smem, s, p);
+  }
+  const int64_t tiles = (static_cast<int64_t>(p.T) + kTileTokens - 1) / kTileTokens;
+  const size_t sums = sizeof(float) * kTile * (kAdWarps + 4);
+  p.v_ld = wide_v_stride(p.r_max);
+  e = allow_smem<shrink_kernel<NT, VEC>>(sums);
+  if (e != cudaSuccess) return e;
+  e = launch(shrink_kernel<NT, VEC>, tiles * kAdCluster, kAdCluster, sums, s, p);
+  if (e != cudaSuccess) return e;
+  // two blocks an SM up to rank 64
+  constexpr int kSteps = MULTI ? 0 : NT == 8 ? 2 : 1, kStages = MULTI ? 3 : 4;
+  const size_t smem = kStages * (kTileTokens * kBlk * (F32 ? 4 : 2) +
+                                 kBlk * 2 * (kSteps ? 32 * kSteps : p.r32));
+  e = allow_smem<expand_kernel<kSteps, F32, VEC, kStages>>(smem);
+  if (e != cudaSuccess) return e;
+  // narrower tiles while they do not fill the GPU
+  p.tile_rows = 512;
+  while (p.tile_rows > kBlk && tiles * ((p.rows + p.tile_rows - 1) / p.tile_rows) < 4 * n_sm)
+    p.tile_rows /= 2;
+  const int64_t blocks = tiles * ((p.rows + p.tile_rows - 1) / p.tile_rows);
+  if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  return launch(expand_kernel<kSteps, F32, VEC, kStages>, blocks, 1, smem, s, p);
+}
+
+template <bool F32, bool VEC>
+cudaError_t launch_rank(const AdapterParams& p, int n_sm, cudaStream_t s) {
+  if (p.r_max <= 16) return launch_shape<2, false, F32, VEC>(p, n_sm, s);
+  if (p.r_max <= 32) return launch_shape<4, false, F32, VEC>(p, n_sm, s);
+  if (p.r_max <= 64) return launch_shape<8, false, F32, VEC>(p, n_sm, s);
+  return launch_shape<8, true, F32, VEC>(p, n_sm, s);
 }
 
 bool aligned_to(const void* p, uintptr_t bytes) {
@@ -503,12 +1054,19 @@ bool aligned_to(const void* p, uintptr_t bytes) {
 }  // namespace
 }  // namespace pw
 
+extern "C" int64_t pw_adapters_workspace_bytes(int32_t T, int32_t max_rank, int32_t y_type) {
+  if (T <= pw::kNarrow || max_rank < 1 || max_rank > PW_MAX_ADAPTER_RANK) return 0;
+  const int64_t tiles = (static_cast<int64_t>(T) + pw::kTileTokens - 1) / pw::kTileTokens;
+  return tiles * pw::tile_bytes(y_type == PW_F32 ? 3 : 2, pw::wide_v_stride(max_rank));
+}
+
 extern "C" pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const uint16_t* d_a,
                                    const uint16_t* d_b, const int32_t* d_ids,
                                    const int32_t* d_ranks, const float* d_scale,
                                    int32_t n_adapters, int32_t max_rank, int32_t T, int32_t cols,
                                    int32_t rows, const void* d_base, int64_t base_stride,
                                    void* d_y, int32_t y_type, int64_t y_stride,
+                                   void* d_workspace, int64_t workspace_bytes,
                                    pw_stream_t stream) {
   using namespace pw;
   auto bad = [](const char* msg) { return record_error(PW_ERR_INVALID_ARG, msg); };
@@ -531,7 +1089,13 @@ extern "C" pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const 
       !aligned_to(d_ranks, 4) || !aligned_to(d_scale, 4) || !aligned_to(d_base, size) ||
       !aligned_to(d_y, size))
     return bad("pw_adapters: buffers must be aligned to their elements");
+  if (workspace_bytes < pw_adapters_workspace_bytes(T, max_rank, y_type) ||
+      (pw_adapters_workspace_bytes(T, max_rank, y_type) > 0 &&
+       (!d_workspace || !aligned_to(d_workspace, 16))))
+    return bad("pw_adapters: the workspace is smaller than pw_adapters_workspace_bytes, or not 16-byte "
+               "aligned");
   AdapterParams p{};
+  p.ws = static_cast<uint8_t*>(d_workspace);
   p.x = d_x;
   p.a = d_a;
   p.b = d_b;
@@ -548,21 +1112,23 @@ extern "C" pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const 
   p.T = T;
   p.cols = cols;
   p.rows = rows;
-  p.y_f32 = y_type == PW_F32;
-  p.vec_x = cols % 8 == 0 && x_stride % 8 == 0 && aligned_to(d_x, 16) && aligned_to(d_a, 16);
-  p.vec_b = max_rank % 4 == 0 && aligned_to(d_b, 8);
-  p.vec_y = rows % 4 == 0 && y_stride % 4 == 0 && aligned_to(d_y, 4 * size) &&
-            (!d_base || (base_stride % 4 == 0 && aligned_to(d_base, 4 * size)));
-  // v's rows in shared memory: whole 16-rank steps; 32 or 96 bytes modulo 128
-  // apart, so that the four rows of half a warp's 8-byte loads take all banks
-  const int r16 = (max_rank + 15) / 16 * 16;
-  p.v_ld = r16 % 32 == 0 ? r16 + 16 : r16;
-  int R = 1;
-  while (R < 16 && R * 37 < T) R *= 2;
-  const bool wide = T >= 2048;
-  p.R = wide ? 64 : R;
+  // every row of every matrix 16-byte aligned and a multiple of 16 bytes
+  const int64_t per16 = 16 / static_cast<int64_t>(size);
+  const bool vec = cols % 8 == 0 && x_stride % 8 == 0 && aligned_to(d_x, 16) && aligned_to(d_a, 16) &&
+                   max_rank % 8 == 0 && aligned_to(d_b, 16) && rows % per16 == 0 &&
+                   y_stride % per16 == 0 && aligned_to(d_y, 16) &&
+                   (!d_base || (base_stride % per16 == 0 && aligned_to(d_base, 16)));
+  p.v_ld = v_stride(max_rank);
+  p.r32 = (max_rank + 31) / 32 * 32;
+  p.n_terms = y_type == PW_F32 ? 3 : 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = wide ? launch_rank<4>(p, s) : launch_rank<1>(p, s);
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return record_error(PW_ERR_CUDA, cudaGetErrorString(e));
+  e = y_type == PW_F32
+                            ? (vec ? launch_rank<true, true>(p, n_sm, s) : launch_rank<true, false>(p, n_sm, s))
+                            : (vec ? launch_rank<false, true>(p, n_sm, s) : launch_rank<false, false>(p, n_sm, s));
   if (e != cudaSuccess) return record_error(PW_ERR_CUDA, cudaGetErrorString(e));
   return PW_OK;
 }

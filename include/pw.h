@@ -449,14 +449,19 @@ pw_status_t pw_token_logprobs(const void* d_logits, int32_t logits_type, int64_t
  * need only their elements' alignment; 16-byte aligned rows are read in
  * 16-byte pieces.  Accumulation is fp32, A_a x_t enters the second product
  * with 24 (y fp32) or 16 (y bf16) significant bits.  T >= 0,
- * 1 <= max_rank <= PW_MAX_ADAPTER_RANK.  One launch, no workspace. */
+ * 1 <= max_rank <= PW_MAX_ADAPTER_RANK.  d_workspace: device memory of
+ * workspace_bytes >= pw_adapters_workspace_bytes (0 up to 512 tokens, then
+ * NULL is accepted), 16-byte aligned, used by this call alone until its work
+ * is done; its contents need not be set or kept. */
 #define PW_MAX_ADAPTER_RANK 256
 #define PW_MAX_ADAPTERS 4194303
 pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const uint16_t* d_a,
                         const uint16_t* d_b, const int32_t* d_ids, const int32_t* d_ranks,
                         const float* d_scale, int32_t n_adapters, int32_t max_rank, int32_t T,
                         int32_t cols, int32_t rows, const void* d_base, int64_t base_stride,
-                        void* d_y, int32_t y_type, int64_t y_stride, pw_stream_t stream);
+                        void* d_y, int32_t y_type, int64_t y_stride, void* d_workspace,
+                        int64_t workspace_bytes, pw_stream_t stream);
+int64_t pw_adapters_workspace_bytes(int32_t T, int32_t max_rank, int32_t y_type);
 
 /* pw_moe_forward of a pre-norm block: y = MoE(x') with x' the bf16 y of
  * pw_add_rms_norm(x, residual, norm_w, eps); residual_out as there.  d_x bf16
