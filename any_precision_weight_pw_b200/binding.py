@@ -219,20 +219,30 @@ def plan_release(blocks, target_bytes: int):
 
 # ---- around a projection ----------------------------------------------------
 # These calls take views with a row stride, run on the tensors' device and
-# check every tensor; a refused argument raises PwError(PW_ERR_INVALID_ARG)
-# before anything is enqueued.
+# check every tensor they are given; a refused argument raises
+# PwError(PW_ERR_INVALID_ARG) before anything is enqueued.  They take a few
+# microseconds on the GPU for a decode batch, so the host side is kept short:
+# names are bound once, and tensors made here are not checked again.
 
-_types = None
+_torch = None
 
 
-def _type_codes():
-    """torch dtype -> pw_dtype_t (int16 / uint8 stand for bf16 / e4m3 bit patterns)."""
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.float32: 0, torch.bfloat16: 1, torch.int16: 1, torch.float16: 2,
-                  torch.float8_e4m3fn: 3, torch.uint8: 3}
-    return _types
+def _bind() -> None:
+    """Module names used on every call: torch, its types' pw_dtype_t codes
+    (int16 / uint8 stand for bf16 / e4m3 bit patterns), the current stream."""
+    global _torch, _types, _f32, _i32, _bf16, _bf16_like, _like
+    global _current_device, _current_stream
+    import torch
+    _f32, _i32, _bf16, _bf16_like = (torch.float32, torch.int32, torch.bfloat16,
+                                     (torch.bfloat16, torch.int16))
+    _types = {_f32: 0, _bf16: 1, torch.int16: 1, torch.float16: 2, torch.float8_e4m3fn: 3,
+              torch.uint8: 3}
+    _like = torch.empty_like  # the shortest way to a new tensor
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    # the handle alone: torch.cuda.current_stream() makes a Stream object, 3 us
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _torch = torch
 
 
 def _refuse(message: str):
@@ -241,7 +251,7 @@ def _refuse(message: str):
 
 def _rows(t, name: str, shape, device: int, types) -> int:
     """Check a [rows][columns] tensor with contiguous rows; its row stride."""
-    if t.dim() != 2 or t.shape != shape:
+    if t.shape != shape:
         _refuse("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.get_device() != device:
         _refuse("%s: on another device than the other tensors" % name)
@@ -268,14 +278,19 @@ def _flat(t, name: str, shape, device: int, dtypes) -> int:
     return t.data_ptr()
 
 
-def _on_stream(fn, stream, tensors, *args, **kw):
-    """fn on `stream`, outputs allocated there and the inputs' memory kept
-    from reuse until the work on it is done."""
-    import torch
-    with torch.cuda.stream(stream):
-        out = fn(*args, **kw)
-    for t in tensors:
-        if t is not None:
+def _elsewhere(fn, dev: int, stream, *args):
+    """fn on `stream`, or on another device's current one.  On a stream,
+    outputs are allocated there, and the tensors' memory is kept from reuse
+    until the work on it is done."""
+    if stream is None:
+        with _torch.cuda.device(dev):
+            return fn(*args)
+    if stream.device.index != dev:
+        _refuse("stream: on another device than the tensors")
+    with _torch.cuda.stream(stream):
+        out = fn(*args)
+    for t in args:
+        if isinstance(t, _torch.Tensor):
             t.record_stream(stream)
     return out
 
@@ -290,47 +305,51 @@ def add_rms_norm(x, weight, eps: float, residual=None, residual_out=None, y=None
     columns (scale_group 128, [T][ceil(H / 128)]), y ~ scale * q.
     residual_out may be the residual itself.  Returns (y, scales or None,
     residual_out or None)."""
-    import torch
-    if not x.is_cuda or x.dim() != 2:
-        _refuse("x: a CUDA tensor [T][H] is needed")
+    if _torch is None:
+        _bind()
     dev = x.get_device()
-    if stream is not None:
-        return _on_stream(add_rms_norm, stream, (x, weight, residual, residual_out, y, scales), x,
-                          weight, eps, residual, residual_out, y, scales, y_type, scale_group)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return add_rms_norm(x, weight, eps, residual, residual_out, y, scales, y_type,
-                                scale_group)
-    codes = _type_codes()
+    if dev < 0 or x.dim() != 2:
+        _refuse("x: a CUDA tensor [T][H] is needed")
+    if stream is not None or dev != _current_device():
+        return _elsewhere(add_rms_norm, dev, stream, x, weight, eps, residual, residual_out, y,
+                          scales, y_type, scale_group)
     T, H = shape = x.shape
     x_ld = _rows(x, "x", shape, dev, (0, 1))
-    w = _flat(weight, "weight", (H,), dev, (torch.bfloat16, torch.float32, torch.int16))
-    r_ld = ro_ld = r_code = 0
+    w = _flat(weight, "weight", (H,), dev, (_bf16, _f32, _torch.int16))
+    res = r_ld = r_out = ro_ld = r_code = 0
     if residual is not None:
         r_ld = _rows(residual, "residual", shape, dev, (0, 1))
-        r_code = codes[residual.dtype]
+        r_code, res = _types[residual.dtype], residual.data_ptr()
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
-        ro_ld = _rows(residual_out, "residual_out", shape, dev, (r_code,))
+            residual_out, ro_ld = _like(residual), H
+        else:
+            ro_ld = _rows(residual_out, "residual_out", shape, dev, (r_code,))
+        r_out = residual_out.data_ptr()
     elif residual_out is not None:
         _refuse("residual_out: needs a residual")
     if y is None:
-        y = torch.empty(shape, dtype=y_type or torch.bfloat16, device=x.device)
-    elif y_type is not None and codes.get(y.dtype) != codes.get(y_type):
-        _refuse("y: type %s, y_type %s" % (y.dtype, y_type))
-    y_ld = _rows(y, "y", shape, dev, (1, 3))
-    y_code = codes[y.dtype]
+        y, y_ld = _like(x, dtype=y_type or _bf16), H
+    else:
+        if y_type is not None and _types.get(y.dtype) != _types.get(y_type):
+            _refuse("y: type %s, y_type %s" % (y.dtype, y_type))
+        y_ld = _rows(y, "y", shape, dev, (1, 3))
+    y_code = _types.get(y.dtype)
+    s = 0
     if y_code == 3:
         want = (T, 1 if scale_group == 0 else -(-H // 128))
         if scales is None:
-            scales = torch.empty(want, dtype=torch.float32, device=x.device)
+            scales = x.new_empty(want, dtype=_f32)
+            s = scales.data_ptr()
+        else:
+            s = _flat(scales, "scales", want, dev, (_f32,))
+    elif y_code != 1:
+        _refuse("y: type %s" % y.dtype)
     elif scales is not None:
         _refuse("scales: only with an 8-bit y")
-    s = _flat(scales, "scales", want, dev, (torch.float32,)) if y_code == 3 else 0
-    status = lib().pw_add_rms_norm(x.data_ptr(), codes[x.dtype], x_ld, _ptr(residual), r_code,
-                                   r_ld, w, codes[weight.dtype], eps, T, H, _ptr(residual_out),
-                                   ro_ld, y.data_ptr(), y_code, y_ld, s, scale_group,
-                                   torch.cuda.current_stream().cuda_stream)
+    status = (_lib or lib()).pw_add_rms_norm(x.data_ptr(), _types[x.dtype], x_ld, res, r_code, r_ld,
+                                             w, _types[weight.dtype], eps, T, H, r_out, ro_ld,
+                                             y.data_ptr(), y_code, y_ld, s, scale_group,
+                                             _current_stream(dev))
     if status:
         check(status)
     return y, scales, residual_out
@@ -343,41 +362,47 @@ def token_logprobs(logits, tokens=None, n_top: int = 0, logprob=None, entropy=No
     and the n_top best alternatives (largest first, ties to the lower index).
     Returns (logprob fp32 [T] or None, entropy fp32 [T], top_idx int32
     [T][n_top] or None, top_logprob fp32 [T][n_top] or None)."""
-    import torch
-    if not logits.is_cuda or logits.dim() != 2:
-        _refuse("logits: a CUDA tensor [T][V] is needed")
+    if _torch is None:
+        _bind()
     dev = logits.get_device()
-    if stream is not None:
-        return _on_stream(token_logprobs, stream,
-                          (logits, tokens, logprob, entropy, top_idx, top_logprob), logits, tokens,
-                          n_top, logprob, entropy, top_idx, top_logprob)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return token_logprobs(logits, tokens, n_top, logprob, entropy, top_idx, top_logprob)
-    codes = _type_codes()
+    if dev < 0 or logits.dim() != 2:
+        _refuse("logits: a CUDA tensor [T][V] is needed")
+    if stream is not None or dev != _current_device():
+        return _elsewhere(token_logprobs, dev, stream, logits, tokens, n_top, logprob, entropy,
+                          top_idx, top_logprob)
     T, V = shape = logits.shape
     ld = _rows(logits, "logits", shape, dev, (0, 1, 2))
-    f32, i32 = (torch.float32,), (torch.int32,)
-
-    def out(t, name, want, dtypes):
-        if t is None:
-            t = torch.empty(want, dtype=dtypes[0], device=logits.device)
-        return t, _flat(t, name, want, dev, dtypes)
-
     tok = lp = ti = tl = 0
     if tokens is not None:
-        tok = _flat(tokens, "tokens", (T,), dev, i32)
-        logprob, lp = out(logprob, "logprob", (T,), f32)
+        tok = _flat(tokens, "tokens", (T,), dev, (_i32,))
+        if logprob is None:
+            logprob = _like(tokens, dtype=_f32)
+            lp = logprob.data_ptr()
+        else:
+            lp = _flat(logprob, "logprob", (T,), dev, (_f32,))
     elif logprob is not None:
         _refuse("logprob: needs tokens")
-    entropy, ent = out(entropy, "entropy", (T,), f32)
+    if entropy is None:
+        entropy = _like(logprob) if lp else logits.new_empty((T,), dtype=_f32)
+        ent = entropy.data_ptr()
+    else:
+        ent = _flat(entropy, "entropy", (T,), dev, (_f32,))
     if n_top > 0:
-        top_idx, ti = out(top_idx, "top_idx", (T, n_top), i32)
-        top_logprob, tl = out(top_logprob, "top_logprob", (T, n_top), f32)
+        want = (T, n_top)
+        if top_idx is None:
+            top_idx = logits.new_empty(want, dtype=_i32)
+            ti = top_idx.data_ptr()
+        else:
+            ti = _flat(top_idx, "top_idx", want, dev, (_i32,))
+        if top_logprob is None:
+            top_logprob = _like(top_idx, dtype=_f32)
+            tl = top_logprob.data_ptr()
+        else:
+            tl = _flat(top_logprob, "top_logprob", want, dev, (_f32,))
     elif top_idx is not None or top_logprob is not None:
         _refuse("top_idx, top_logprob: need n_top > 0")
-    status = lib().pw_token_logprobs(logits.data_ptr(), codes[logits.dtype], ld, T, V, tok, n_top,
-                                     lp, ent, ti, tl, torch.cuda.current_stream().cuda_stream)
+    status = (_lib or lib()).pw_token_logprobs(logits.data_ptr(), _types[logits.dtype], ld, T, V,
+                                               tok, n_top, lp, ent, ti, tl, _current_stream(dev))
     if status:
         check(status)
     return logprob, entropy, top_idx, top_logprob
@@ -392,45 +417,42 @@ def add_adapters(x, a, b, ids, base=None, scale=None, ranks=None, y=None, y_type
     ids int32 [T]; scale fp32 [n] and ranks int32 [n] on the device
     (optional); base [T][rows] fp32 or bf16 (optional; may be y); y of base's
     type (y_type, default fp32, without a base).  Returns y."""
-    import torch
-    if not x.is_cuda or x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
-        _refuse("CUDA tensors x [T][cols], a [n][max_rank][cols], b [n][rows][max_rank] are needed")
+    if _torch is None:
+        _bind()
     dev = x.get_device()
-    if stream is not None:
-        return _on_stream(add_adapters, stream, (x, a, b, ids, base, scale, ranks, y), x, a, b, ids,
-                          base, scale, ranks, y, y_type)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return add_adapters(x, a, b, ids, base, scale, ranks, y, y_type)
-    codes = _type_codes()
-    T, cols = x.shape
+    if dev < 0 or x.dim() != 2 or a.dim() != 3 or b.dim() != 3 or ids is None:
+        _refuse("CUDA tensors x [T][cols], a [n][max_rank][cols], b [n][rows][max_rank] and ids [T] "
+                "are needed")
+    if stream is not None or dev != _current_device():
+        return _elsewhere(add_adapters, dev, stream, x, a, b, ids, base, scale, ranks, y, y_type)
+    T, cols = shape = x.shape
     n, rows, r = b.shape
-    bf16 = (torch.bfloat16, torch.int16)
-    if ids is None:
-        _refuse("ids: an adapter index for each token is needed")
-    x_ld = _rows(x, "x", x.shape, dev, (1,))
-    pa = _flat(a, "a", (n, r, cols), dev, bf16)
-    pb = _flat(b, "b", b.shape, dev, bf16)
-    pi = _flat(ids, "ids", (T,), dev, (torch.int32,))
-    pr = _flat(ranks, "ranks", (n,), dev, (torch.int32,))
-    ps = _flat(scale, "scale", (n,), dev, (torch.float32,))
+    x_ld = _rows(x, "x", shape, dev, (1,))
+    pa = _flat(a, "a", (n, r, cols), dev, _bf16_like)
+    pb = _flat(b, "b", (n, rows, r), dev, _bf16_like)
+    pi = _flat(ids, "ids", (T,), dev, (_i32,))
+    pr = _flat(ranks, "ranks", (n,), dev, (_i32,))
+    ps = _flat(scale, "scale", (n,), dev, (_f32,))
     shape, base_ld, pbase = (T, rows), 0, 0
     if base is not None:
         base_ld = _rows(base, "base", shape, dev, (0, 1))
         pbase = base.data_ptr()
     if y is None:
-        dtype = base.dtype if base is not None else y_type or torch.float32
-        y = torch.empty(shape, dtype=dtype, device=x.device)
-    y_ld = _rows(y, "y", shape, dev, (0, 1) if base is None else (codes[base.dtype],))
-    if y_type is not None and codes.get(y_type) != codes[y.dtype]:
+        y_ld = rows
+        y = _like(base) if base is not None else x.new_empty(shape, dtype=y_type or _f32)
+    else:
+        y_ld = _rows(y, "y", shape, dev, (0, 1) if base is None else (_types[base.dtype],))
+    y_code = _types.get(y.dtype)
+    if y_type is not None and _types.get(y_type) != y_code:
         _refuse("y: type %s, y_type %s" % (y.dtype, y_type))
-    work, size = 0, lib().pw_adapters_workspace_bytes(T, r, codes[y.dtype])
+    L = _lib or lib()
+    work, size = 0, L.pw_adapters_workspace_bytes(T, r, y_code or 0)
     if size:
-        keep = torch.empty(size, dtype=torch.uint8, device=x.device)
+        keep = x.new_empty((size,), dtype=_torch.uint8)
         work = keep.data_ptr()
-    status = lib().pw_adapters(x.data_ptr(), x_ld, pa, pb, pi, pr, ps, n, r, T, cols, rows, pbase,
-                               base_ld, y.data_ptr(), codes[y.dtype], y_ld, work, size,
-                               torch.cuda.current_stream().cuda_stream)
+    status = L.pw_adapters(x.data_ptr(), x_ld, pa, pb, pi, pr, ps, n, r, T, cols, rows, pbase,
+                           base_ld, y.data_ptr(), -1 if y_code is None else y_code, y_ld, work, size,
+                           _current_stream(dev))
     if status:
         check(status)
     return y

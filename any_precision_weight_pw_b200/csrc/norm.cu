@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
   const int tpr = p.tpr, lane_r = threadIdx.x % tpr, rows_blk = blockDim.x / tpr;
   pdl_wait();
   // the weights stay in registers over the rows where there is room
-  constexpr bool kHold = N * M <= 16;
+  constexpr bool kHold = N * M <= 8;
   float wv[kHold ? M : 1][N];
   auto load_w = [&](int j, float* w) {
     const int c = (j * tpr + lane_r) * N;
@@ -197,31 +197,35 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
 #pragma unroll
     for (int j = 0; j < M; ++j) load_w(j, wv[j]);
   }
+  // the next row's loads are in flight while a row is reduced and written
+  Raw<XT, N> rx[M];
+  Raw<RT, N> rr[M];
+  auto load_row = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int c = (j * tpr + lane_r) * N;
+      if (row < p.T && c < p.H) {
+        rx[j].load(p.x, row * p.x_ld + c);
+        rr[j].load(p.res, row * p.res_ld + c);
+      } else {
+        rx[j].zero();
+        rr[j].zero();
+      }
+    }
+  };
   int parity = 0;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * rows_blk;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * rows_blk + threadIdx.x / tpr;
+  load_row(row);
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows_blk; row0 < p.T;
-       row0 += static_cast<int64_t>(gridDim.x) * rows_blk, parity ^= 1) {
-    const int64_t row = row0 + threadIdx.x / tpr;
+       row0 += row_step, row += row_step, parity ^= 1) {
     const bool live = row < p.T;  // a whole warp agrees: rows sharing a block are a warp each
     float h[M][N];
-    {
-      Raw<XT, N> rx[M];
-      Raw<RT, N> rr[M];
 #pragma unroll
-      for (int j = 0; j < M; ++j) {
-        const int c = (j * tpr + lane_r) * N;
-        if (live && c < p.H) {
-          rx[j].load(p.x, row * p.x_ld + c);
-          rr[j].load(p.res, row * p.res_ld + c);
-        } else {
-          rx[j].zero();
-          rr[j].zero();
-        }
-      }
+    for (int j = 0; j < M; ++j)
 #pragma unroll
-      for (int j = 0; j < M; ++j)
-#pragma unroll
-        for (int k = 0; k < N; ++k) h[j][k] = rx[j].get(k) + rr[j].get(k);
-    }
+      for (int k = 0; k < N; ++k) h[j][k] = rx[j].get(k) + rr[j].get(k);
+    load_row(row + row_step);
     if constexpr (!std::is_same<RT, None>::value) {
       if (p.res_out && live) {
 #pragma unroll
@@ -349,7 +353,7 @@ cudaError_t launch_shape(NormParams p, int n_sm, cudaStream_t s) {
   const int rows_blk = p.tpr == 32 ? 4 : 1;
   const int threads = p.tpr * rows_blk;
   int64_t grid = (static_cast<int64_t>(p.T) + rows_blk - 1) / rows_blk;
-  const int64_t most = static_cast<int64_t>(n_sm) * (2048 / threads);
+  const int64_t most = static_cast<int64_t>(n_sm) * (kNormThreads / threads);
   if (grid > most) grid = most;
   const size_t smem = (N == 1 && OUT == kOutE4m3Group) ? sizeof(float) * 2 * M * (p.tpr >> 5) : 0;
   return launch_pdl(norm_kernel<XT, RT, OUT, N, M>, dim3(static_cast<unsigned>(grid)), dim3(threads),
