@@ -60,8 +60,8 @@ struct AdapterParams {
   int per_window;  // clusters of a full window (few tokens)
   int v_ld;        // bf16 elements between the rows of v
   int n_terms;     // bf16 terms of v
-  int tile_rows;   // many tokens: rows of an expand tile
   int r32;         // max_rank in whole 32s
+  int tile_rows;   // many tokens: rows of an expand tile
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -124,24 +124,22 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int cols) {
   for (int i = 0; i < 8; ++i) w[i] = i < count ? __ldg(p + i) : 0u;
   return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
 }
-// the first `count` of 4 bf16, zero past them; VEC: 8-byte aligned, and a whole
-// row of B follows a multiple of 4 ranks
+// 8 bf16 from rank k of a row of B, zero from `rank` on; VEC: k is 16-byte
+// aligned in a row of whole 16-byte pieces
 template <bool VEC>
-__device__ __forceinline__ uint2 load4(const uint16_t* p, int count) {
-  if (count <= 0) return make_uint2(0, 0);
-  if constexpr (VEC) {
-    uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    if (count < 4) {
-      v.y &= count == 3 ? 0xffffu : 0u;
-      v.x &= count == 1 ? 0xffffu : 0xffffffffu;
-    }
-    return v;
-  } else {
-    uint32_t w[4];
+__device__ __forceinline__ uint4 load_ranks(const uint16_t* row, int k, int rank) {
+  if constexpr (!VEC) return load8<false>(row, k, rank);
+  const int count = rank - k;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (count > 0) v = __ldg(reinterpret_cast<const uint4*>(row + k));
+  if (rank & 7) {  // the same for the warp
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = i < count ? __ldg(p + i) : 0u;
-    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    for (int i = 0; i < 4; ++i)
+      w[i] &= count >= 2 * i + 2 ? 0xffffffffu : count == 2 * i + 1 ? 0xffffu : 0u;
+    v = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  return v;
 }
 
 __device__ __forceinline__ float bf16_value(uint16_t b) {
@@ -254,8 +252,9 @@ __device__ __forceinline__ uint32_t next_term(float (&v)[2]) {
 
 // 16 tokens x 16 rows of the second product.  MMA column g of tile j is row
 // o + 4 (g / 2) + 2 j + g % 2: a lane then holds rows 4q..4q+3, whole 16-byte
-// accesses of base and y.
-// F32: type of base and y.  VEC: every access is aligned and rows % 4 == 0.
+// accesses of base and y.  A lane holds ranks 8q..8q+7 of each 32 (two MMA
+// steps), whole 16-byte accesses of B and v.
+// KS: 32-rank steps.  F32: type of base and y.  VEC: every access is aligned.
 template <int KS, bool F32, bool VEC>
 struct ExpandTile {
   static constexpr int kTerms = F32 ? 3 : 2;
@@ -266,9 +265,10 @@ struct ExpandTile {
   struct Lane {
     const E* base[2];
     E* y[2];
-    const uint16_t* b;
+    const uint16_t* b;  // row 4 (g / 2) + g % 2 of the adapter
     const uint16_t* v;
     bool on[2], any_base;
+    int left;           // rows from this lane's first on
     __device__ __forceinline__ Lane(const AdapterParams& p, const Piece& pc, const int* tok,
                                     const uint16_t* v_rows) {
       const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -280,18 +280,18 @@ struct ExpandTile {
         y[h] = static_cast<E*>(p.y) + t * p.y_ld + 4 * q;
       }
       any_base = p.base != nullptr;
-      b = p.b + (static_cast<int64_t>(max(pc.adapter, 0)) * p.rows + 4 * (g >> 1) + (g & 1)) * p.r_max +
-          4 * q;
-      v = v_rows + g * p.v_ld + 4 * q;
+      b = p.b + (static_cast<int64_t>(max(pc.adapter, 0)) * p.rows + 4 * (g >> 1) + (g & 1)) * p.r_max;
+      v = v_rows + g * p.v_ld + 8 * q;
+      left = p.rows - 4 * q;
     }
   };
 
   Raw4 add[2];     // [token half]: base as it lies in memory
-  uint2 w[KS][2];  // B, a 16-rank step each
+  uint4 w[KS][2];  // B
 
-  // base, and B of ranks [0, 16 KS)
+  // base, and B of ranks [0, 32 KS)
   __device__ __forceinline__ void load(const AdapterParams& p, const Piece& pc, const Lane& l, int ob) {
-    const int left = p.rows - ob * 16 - 4 * static_cast<int>(threadIdx.x & 3);
+    const int left = l.left - ob * 16;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const E* src = l.base[h] + ob * 16;
@@ -316,37 +316,40 @@ struct ExpandTile {
   __device__ __forceinline__ void load_b(const AdapterParams& p, const Piece& pc, const Lane& l,
                                          int ob, int k0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int ro = ob * 16 + 4 * (g >> 1) + (g & 1), count = pc.rank - k0 - 4 * q;
+    const int rows = p.rows - ob * 16 - 4 * (g >> 1) - (g & 1);
+    const uint16_t* src = l.b + static_cast<int64_t>(ob * 16) * p.r_max;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint16_t* src = l.b + static_cast<int64_t>(ob * 16 + 2 * j) * p.r_max + k0;
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
-        w[ks][j] = load4<VEC>(src + 16 * ks, ro + 2 * j < p.rows ? count - 16 * ks : 0);
-    }
+        w[ks][j] = load_ranks<VEC>(src + 2 * j * p.r_max, k0 + 32 * ks + 8 * q,
+                                   rows > 2 * j ? pc.rank : 0);
   }
   // left: ranks from k0 on
   __device__ __forceinline__ void multiply(const AdapterParams& p, const Lane& l, int v_plane, int k0,
                                            int left, float (&acc)[2][4]) const {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      if (16 * ks >= left) break;
+      if (32 * ks >= left) break;
 #pragma unroll
       for (int t = 0; t < kTerms; ++t) {
-        const uint16_t* vp = l.v + t * v_plane + k0 + 16 * ks;
-        const uint2 lo = *reinterpret_cast<const uint2*>(vp);
-        const uint2 hi = *reinterpret_cast<const uint2*>(vp + 8 * p.v_ld);
+        const uint16_t* vp = l.v + t * v_plane + k0 + 32 * ks;
+        const uint4 lo = *reinterpret_cast<const uint4*>(vp);
+        const uint4 hi = *reinterpret_cast<const uint4*>(vp + 8 * p.v_ld);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) mma16816(acc[j], lo.x, hi.x, lo.y, hi.y, w[ks][j].x, w[ks][j].y);
+        for (int j = 0; j < 2; ++j) {
+          mma16816(acc[j], lo.x, hi.x, lo.y, hi.y, w[ks][j].x, w[ks][j].y);
+          mma16816(acc[j], lo.z, hi.z, lo.w, hi.w, w[ks][j].z, w[ks][j].w);
+        }
       }
     }
   }
-  __device__ __forceinline__ void store(const AdapterParams& p, const Lane& l, int ob,
-                                        const float (&acc)[2][4]) const {
-    const int left = p.rows - ob * 16 - 4 * static_cast<int>(threadIdx.x & 3);
+  __device__ __forceinline__ void store(const Lane& l, int ob, const float (&acc)[2][4]) const {
+    const int left = l.left - ob * 16;
+    if (left <= 0) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (!l.on[h] || left <= 0) continue;
+      if (!l.on[h]) continue;
       const Raw4 r = add[h];
       float v[4];
       if constexpr (F32) {
@@ -380,7 +383,7 @@ struct ExpandTile {
 };
 
 // The second product of one piece over 16-row blocks ob, ob + step, ... < ob1,
-// D tiles in flight.  Ranks above 16 KS take further steps (MULTI).
+// D tiles in flight.  Ranks above 32 KS take further steps (MULTI).
 template <int D, bool MULTI, int KS, bool F32, bool VEC>
 struct Expand {
   using Tile = ExpandTile<KS, F32, VEC>;
@@ -401,11 +404,11 @@ struct Expand {
         float acc[2][4] = {};
         t[d].multiply(p, l, v_plane, 0, pc.rank, acc);
         if (MULTI)
-          for (int k0 = 16 * KS; k0 < pc.rank; k0 += 16 * KS) {
+          for (int k0 = 32 * KS; k0 < pc.rank; k0 += 32 * KS) {
             t[d].load_b(p, pc, l, ob, k0);
             t[d].multiply(p, l, v_plane, k0, pc.rank - k0, acc);
           }
-        t[d].store(p, l, ob, acc);
+        t[d].store(l, ob, acc);
         if (ob + D * step < ob1) t[d].load(p, pc, l, ob + D * step);
       }
     }
@@ -418,7 +421,7 @@ template <int NT, bool MULTI, bool F32, bool VEC>
 __global__ void __launch_bounds__(kAdThreads, 2) adapter_kernel(const AdapterParams p) {
   constexpr int kChunk = 8 * NT;       // ranks of a shrink step
   constexpr int kTile = 16 * kChunk;   // sums of a piece and step
-  constexpr int KS = NT / 2;
+  constexpr int KS = NT == 8 ? 2 : 1;
   extern __shared__ __align__(16) uint8_t smem[];
   float* red = reinterpret_cast<float*>(smem);  // [8 warps][16][kChunk]
   float* slots = red + kAdWarps * kTile;        // [1, MULTI 2][8 blocks][16][kChunk]
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(kAdThreads, 2) adapter_kernel(const AdapterPar
 
   using Tile = ExpandTile<KS, F32, VEC>;
   const typename Tile::Lane l(p, pc, tok, vt);
-  Expand<MULTI ? 1 : KS == 4 ? 2 : 4, MULTI, KS, F32, VEC> second;
+  Expand<MULTI ? 1 : KS == 2 ? 3 : 4, MULTI, KS, F32, VEC> second;
   if (pc.rank == 0) second.start(p, pc, l, ob0, ob1, kAdWarps);
   auto shrink = [&](int r0, int step) {
     float acc[NT][4];
@@ -523,21 +526,22 @@ __global__ void __launch_bounds__(kAdThreads, 2) adapter_kernel(const AdapterPar
     cluster_arrive();
     cluster_wait();
     // sums over the blocks; scale v and split it into bf16 terms
-    for (int e = tid * 2; e < kTile; e += kAdThreads * 2) {
+    for (int e = tid * 2; e < pc.len * kChunk; e += kAdThreads * 2) {
       const int row = e / kChunk, k = r0 + e % kChunk;
-      if (k >= p.v_ld) continue;
+      if (k >= p.r32) continue;
       float v[2] = {0.f, 0.f};
-      if (row < pc.len) {
 #pragma unroll
-        for (int c = 0; c < kAdCluster; ++c) {
-          const float2 o = *reinterpret_cast<const float2*>(slot + c * kTile + e);
-          v[0] += o.x, v[1] += o.y;
-        }
-        v[0] *= sc, v[1] *= sc;
+      for (int c = 0; c < kAdCluster; ++c) {
+        const float2 o = *reinterpret_cast<const float2*>(slot + c * kTile + e);
+        v[0] += o.x, v[1] += o.y;
       }
+      v[0] *= sc, v[1] *= sc;
 #pragma unroll
-      for (int t = 0; t < Tile::kTerms; ++t)
-        *reinterpret_cast<uint32_t*>(vt + t * v_plane + row * p.v_ld + k) = next_term(v);
+      for (int t = 0; t < Tile::kTerms; ++t) {
+        uint16_t* d = vt + t * v_plane + row * p.v_ld + k;
+        *reinterpret_cast<uint32_t*>(d) = next_term(v);
+        if (kChunk == 16) *reinterpret_cast<uint32_t*>(d + 16) = 0;
+      }
     }
     __syncthreads();
   };
@@ -985,15 +989,9 @@ cudaError_t launch(K* kernel, int64_t grid, int cluster, size_t smem, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// v's rows in shared memory, in elements.  Few tokens: whole 16-rank steps, 32
-// or 96 bytes modulo 128 apart, so that the four rows of half a warp's 8-byte
-// loads take all banks.  Many: whole 32s, 64 modulo 128 bytes apart, two rows
-// of 16-byte loads.
+// v's rows, in elements: whole 32-rank steps, 64 bytes modulo 128 apart, so
+// that 8 lanes' 16-byte shared-memory loads of two rows take all banks
 int v_stride(int max_rank) {
-  const int r16 = (max_rank + 15) / 16 * 16;
-  return r16 % 32 == 0 ? r16 + 16 : r16;
-}
-int wide_v_stride(int max_rank) {
   const int r32 = (max_rank + 31) / 32 * 32;
   return r32 % 64 == 0 ? r32 + 32 : r32;
 }
@@ -1019,7 +1017,6 @@ cudaError_t launch_shape(AdapterParams p, int n_sm, cudaStream_t s) {
   }
   const int64_t tiles = (static_cast<int64_t>(p.T) + kTileTokens - 1) / kTileTokens;
   const size_t sums = sizeof(float) * kTile * (kAdWarps + 4);
-  p.v_ld = wide_v_stride(p.r_max);
   e = allow_smem<shrink_kernel<NT, VEC>>(sums);
   if (e != cudaSuccess) return e;
   e = launch(shrink_kernel<NT, VEC>, tiles * kAdCluster, kAdCluster, sums, s, p);
@@ -1057,7 +1054,7 @@ bool aligned_to(const void* p, uintptr_t bytes) {
 extern "C" int64_t pw_adapters_workspace_bytes(int32_t T, int32_t max_rank, int32_t y_type) {
   if (T <= pw::kNarrow || max_rank < 1 || max_rank > PW_MAX_ADAPTER_RANK) return 0;
   const int64_t tiles = (static_cast<int64_t>(T) + pw::kTileTokens - 1) / pw::kTileTokens;
-  return tiles * pw::tile_bytes(y_type == PW_F32 ? 3 : 2, pw::wide_v_stride(max_rank));
+  return tiles * pw::tile_bytes(y_type == PW_F32 ? 3 : 2, pw::v_stride(max_rank));
 }
 
 extern "C" pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const uint16_t* d_a,
