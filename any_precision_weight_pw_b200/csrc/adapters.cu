@@ -42,7 +42,7 @@ constexpr int kAdWarps = kAdThreads / 32;
 constexpr int kAdCluster = 8;
 constexpr int kWindow = 256;     // tokens ordered together
 constexpr int kNarrow = 512;     // most tokens of the one-launch path
-constexpr int kTileTokens = 64;  // many tokens: tokens of a cluster / tile
+constexpr int kTileTokens = 64;  // many tokens: tokens of a shrink cluster, of an expand tile
 constexpr int kMaxDevices = 64;
 
 struct AdapterParams {
@@ -62,6 +62,7 @@ struct AdapterParams {
   int n_terms;     // bf16 terms of v
   int r32;         // max_rank in whole 32s
   int tile_rows;   // many tokens: rows of an expand tile
+  int split;       // and blocks of a shrink cluster
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -567,40 +568,139 @@ __host__ __device__ __forceinline__ int64_t tile_bytes(int n_terms, int v_ld) {
   return static_cast<int64_t>(sizeof(TileInfo)) + 2ll * n_terms * kTileTokens * v_ld;
 }
 
-template <int NT, bool VEC>
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred = 0;
+  asm volatile(
+      "{\n.reg .pred P1;\n.reg .b32 r;\nelect.sync r|P1, %1;\nselp.u32 %0, 1, 0, P1;\n}\n"
+      : "=r"(pred)
+      : "r"(0xffffffffu));
+  return pred != 0;
+}
+// K-major operand in 128-byte swizzle: 64 bf16 a row, 8-row groups of 1024
+// bytes, 16-byte piece c of row r at piece c ^ (r & 7).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | 1ull << 16 | 64ull << 32 | 1ull << 46 |
+         2ull << 61;
+}
+__device__ __forceinline__ uint32_t operand_off(int row, int piece) {
+  return (row >> 3) * 1024 + (row & 7) * 128 + ((piece ^ (row & 7)) << 4);
+}
+// bf16 x bf16 -> fp32, M = 128
+__device__ __forceinline__ uint32_t mma_idesc(int n) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | static_cast<uint32_t>(n >> 3) << 17 | 8u << 24;
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
+        "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
+        "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Wait for an mbarrier phase, two seconds at most; a wait that gives up makes
+// the block's later ones give up at once.
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  unsigned long long t0 = 0, t = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok || *gave_up) return;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t0 == 0) t0 = t;
+    if (t - t0 > 2000000000ull) {
+      *gave_up = 1;
+      return;
+    }
+  }
+}
+
+constexpr int kShrinkStages = 5;
+constexpr int kShrinkStage = 2 * 64 * 128;  // bytes: x [64][64], A [64][64]
+constexpr int kTmemCols = 64;               // an accumulator
+
+// v of 64 ordered tokens: a cluster of p.split blocks, each its share of the
+// columns.  Per segment and 64 ranks: D[token][rank] = x [64][64] A^T over the block's
+// 64-column steps on tcgen05, copied four steps ahead.  The MMA has 128 rows;
+// the upper 64 run over the A tile behind x and are not used (the tensor cores
+// have the time: half a percent of it is used).  Partial sums go to the block
+// that owns the tokens, which adds them in rank order.
+template <bool VEC>
 __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterParams p) {
-  constexpr int MT = 4;                // pieces at once, two warps each
-  constexpr int KW = kAdWarps / MT;
-  constexpr int kChunk = 8 * NT;
-  constexpr int kTile = 16 * kChunk;
-  constexpr int kSlot = MT * kTile / kAdCluster;  // sums a block owns
+  constexpr int STAGES = kShrinkStages;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* red = reinterpret_cast<float*>(smem);  // [8 warps][16][kChunk]
-  float* slots = red + kAdWarps * kTile;        // [8 blocks][kSlot]
+  __shared__ __align__(16) float slots[kTileTokens * 64];  // [block][own token][rank]
   __shared__ __align__(16) int s_key[kWindow];
   __shared__ int s_tok[kWindow], s_sid[kWindow];
-  __shared__ Piece s_piece[kTileTokens];
-  __shared__ int s_np;
-  __shared__ uint64_t s_changes;
-
+  __shared__ TileInfo s_info;
+  __shared__ __align__(8) uint64_t s_bar[2];  // products of even and odd steps
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_gave_up;
+  const uint32_t sm = (smem_u32(smem) + 1023) & ~1023u;
+  uint8_t* const smp = smem + (sm - smem_u32(smem));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank());
-  const int cl = blockIdx.x / kAdCluster;
+  const int split = p.split, own = kTileTokens / split;  // blocks; tokens a block owns
+  const int cl = blockIdx.x / split;
   constexpr int kPerWindow = kWindow / kTileTokens;
   const int t0 = cl / kPerWindow * kWindow;
   const int n_win = min(kWindow, p.T - t0);
   const int first = cl % kPerWindow * kTileTokens;
   const int n_rows = min(kTileTokens, n_win - first);  // >= 1 by the grid
+  const uint32_t bar = smem_u32(s_bar);
   cluster_arrive();  // the others' shared memory is live once all have arrived
   pdl_wait();
   pdl_trigger();  // expand's blocks may start; they wait for this grid's end
+  if (tid == 0) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar));
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar + 8));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_gave_up = 0;
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s_tmem)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
   order_window(p, t0, n_win, true, s_key, s_tok, s_sid);
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
   const int* tok = s_tok + first;
   const int* sid = s_sid + first;
   if (warp == 0) {
-    // a piece starts where the adapter changes and at every 16th token of a run
-    uint64_t changes = 0, starts = 0;
-    bool is_start[2];
+    uint64_t changes = 0;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int i = lane + 32 * half;
@@ -610,344 +710,406 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int i = lane + 32 * half;
-      const uint64_t upto = changes & (~0ull >> (63 - i));
-      is_start[half] = i < n_rows && (i - (63 - __clzll(upto))) % 16 == 0;
-      starts |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, is_start[half])) << (32 * half);
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int i = lane + 32 * half;
-      if (!is_start[half]) continue;
-      const uint64_t above = i == 63 ? 0ull : starts & (~0ull << (i + 1));
-      s_piece[__popcll(starts & ((1ull << i) - 1))] = {
+      if (i < n_rows) s_info.tok[i] = tok[i];
+      if (!(changes >> i & 1)) continue;
+      const uint64_t above = i == 63 ? 0ull : changes & (~0ull << (i + 1));
+      s_info.segment[__popcll(changes & ((1ull << i) - 1))] = {
           i, (above ? __ffsll(above) - 1 : n_rows) - i, sid[i], adapter_rank(p, sid[i])};
     }
-    if (lane == 0) {
-      s_np = __popcll(starts);
-      s_changes = changes;
-    }
+    if (lane == 0) s_info.n_segments = __popcll(changes);
   }
   __syncthreads();
-  const int n_pieces = s_np;
   uint8_t* ws = p.ws + cl * tile_bytes(p.n_terms, p.v_ld);
-  if (rank == 0) {
-    TileInfo* info = reinterpret_cast<TileInfo*>(ws);
-    if (tid < n_rows) info->tok[tid] = tok[tid];
-    if (warp == 0) {
-      const uint64_t changes = s_changes;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int i = lane + 32 * half;
-        if (!(changes >> i & 1)) continue;
-        const uint64_t above = i == 63 ? 0ull : changes & (~0ull << (i + 1));
-        info->segment[__popcll(changes & ((1ull << i) - 1))] = {
-            i, (above ? __ffsll(above) - 1 : n_rows) - i, sid[i], adapter_rank(p, sid[i])};
-      }
-      if (lane == 0) info->n_segments = __popcll(changes);
-    }
-  }
+  if (rank == 0 && tid < static_cast<int>(sizeof(TileInfo) / 16))
+    reinterpret_cast<uint4*>(ws)[tid] = reinterpret_cast<const uint4*>(&s_info)[tid];
   uint16_t* vt = reinterpret_cast<uint16_t*>(ws + sizeof(TileInfo));
   const int v_plane = kTileTokens * p.v_ld;
-  const int mp = warp % MT, kw = warp / MT;
-  const int kb_all = (p.cols + 31) / 32;
-  const int kb0 = rank * kb_all / kAdCluster, kb1 = (rank + 1) * kb_all / kAdCluster;
-  cluster_wait();
-  for (int p0 = 0; p0 < n_pieces; p0 += MT) {
-    Piece pc = {0, 0, -1, 0};
-    if (p0 + mp < n_pieces) pc = s_piece[p0 + mp];
-    int r_all = 0;  // largest rank of this pass: the same in all blocks
-    for (int i = p0; i < min(n_pieces, p0 + MT); ++i) r_all = max(r_all, s_piece[i].rank);
-    for (int r0 = 0; r0 < r_all; r0 += kChunk) {
-      float acc[NT][4];
-      shrink_acc<VEC, NT>(p, pc, tok + pc.start, r0, kb0 + kw, kb1, KW, acc);
-      store_acc<NT>(red + warp * kTile, acc);
-      __syncthreads();
-      // each block's sums to the block that owns them
-      for (int e = tid * 4; e < MT * kTile; e += kAdThreads * 4) {
-        const int m = e / kTile, i = e % kTile;
-        float4 s = *reinterpret_cast<const float4*>(red + m * kTile + i);
+  const int kb_all = (p.cols + 63) / 64;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * kb_all / split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * kb_all / split);
+  const int n_segments = s_info.n_segments, n_steps = kb1 - kb0;
+  // The copies run ahead over the passes (a segment's 64 ranks each), with
+  // their own place: rows `row` and row + 32 of both tiles, one 16-byte piece
+  // of each step.
+  const int row = tid >> 3, pc = tid & 7;
+  const uint32_t off = operand_off(row, pc);  // row + 32: 4096 behind; A: 8192
+  int l_seg = 0, l_r0 = 0, l_i = 0, l_stage = 0, l_col = 0;
+  const uint16_t* l_src[4] = {};  // x[row], x[row + 32], A[row], A[row + 32] at this step
+  bool l_on[4] = {};
+  auto issue = [&]() {
+    if (l_i == 0) {
+      while (l_seg < n_segments && s_info.segment[l_seg].rank == 0) ++l_seg;
+      if (l_seg < n_segments) {
+        const Piece sg = s_info.segment[l_seg];
+        l_col = kb0 * 64 + pc * 8;
 #pragma unroll
-        for (int k = 1; k < KW; ++k) {
-          const float4 o = *reinterpret_cast<const float4*>(red + (k * MT + m) * kTile + i);
-          s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+        for (int h = 0; h < 2; ++h) {
+          const int r = row + 32 * h;
+          l_on[h] = r < sg.len;
+          l_src[h] = p.x + tok[sg.start + min(r, sg.len - 1)] * p.x_ld;
+          l_on[2 + h] = l_r0 + r < sg.rank;
+          l_src[2 + h] = p.a + (static_cast<int64_t>(sg.adapter) * p.r_max + l_r0 + r) * p.cols;
         }
-        put4(in_block(smem_u32(slots + rank * kSlot + e % kSlot), e / kSlot), s);
+      }
+    }
+    if (l_seg < n_segments) {
+      const uint32_t at = l_stage * kShrinkStage + off;
+      if (VEC && (kb0 + l_i + 1) * 64 <= p.cols) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if (l_on[h]) cp_async16(sm + at + h * 4096, l_src[h] + l_col);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if (l_on[h]) {
+            if constexpr (VEC)
+              cp_async16(sm + at + h * 4096, l_col < p.cols ? l_src[h] + l_col : p.x,
+                         l_col < p.cols ? 16 : 0);
+            else
+              *reinterpret_cast<uint4*>(smp + at + h * 4096) = load8<false>(l_src[h], l_col, p.cols);
+          }
+      }
+      l_col += 64;
+      l_stage = l_stage + 1 == STAGES ? 0 : l_stage + 1;
+      if (++l_i == n_steps) {
+        l_i = 0;
+        l_r0 += 64;
+        if (l_r0 >= s_info.segment[l_seg].rank) l_r0 = 0, ++l_seg;
+      }
+    }
+    __syncwarp();
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (n_steps > 0)
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) issue();
+  cluster_wait();
+  // Steps so far.  A step's wait comes after the next one's products have been
+  // issued, hence two barriers: one would be two phases ahead of it.
+  uint32_t n_done = 0;
+  auto wait_step = [&](uint32_t n) { mbar_wait(bar + (n & 1) * 8, n >> 1 & 1, &s_gave_up); };
+  int stage = 0;
+  bool sums_read = false;  // an arrive without its wait: this block has read its sums
+  for (int seg = 0; seg < n_segments; ++seg) {
+    const Piece sg = s_info.segment[seg];
+    const float sc = sg.adapter >= 0 && p.scale ? p.scale[sg.adapter] : 1.f;
+    for (int r0 = 0; r0 < sg.rank; r0 += 64) {
+      const int n_r = min(64, sg.rank - r0);
+      const uint32_t idesc = mma_idesc((n_r + 15) / 16 * 16);
+      for (int i = 0; i < n_steps; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();  // the step is there
+        if (warp == 0) {
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t at = sm + stage * kShrinkStage;
+            const uint64_t dx = operand_desc(at), da = operand_desc(at + 8192);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tc_mma(tmem, dx + 2 * k, da + 2 * k, idesc, i | k);
+            asm volatile(
+                "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                    bar + (n_done & 1) * 8)
+                : "memory");
+          }
+          __syncwarp();
+        }
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        if (i > 0) wait_step(n_done - 1);  // its stage takes the next copies
+        ++n_done;
+        issue();
+      }
+      if (n_steps > 0) wait_step(n_done - 1);
+      if (sums_read) cluster_wait();  // the last sums have been read everywhere
+      // token 32 warp + lane of the accumulator to its owner
+      if (warp < 2 && warp * 32 < sg.len) {
+        const int t = warp * 32 + lane;
+        const uint32_t d = in_block(smem_u32(slots + (rank * own + t % own) * 64), t / own);
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (32 * h >= n_r) break;
+          float v[32] = {};
+          if (n_steps > 0) tmem_ld32(tmem + (static_cast<uint32_t>(warp) * 32 << 16) + 32 * h, v);
+          if (t < sg.len)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              put4(d + (32 * h + 4 * j) * 4,
+                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+        }
+        tc_fence_before();
       }
       cluster_arrive();
       cluster_wait();
-      for (int e = tid * 2; e < kSlot; e += kAdThreads * 2) {
-        const int f = rank * kSlot + e;  // of [MT][16][kChunk]
-        const int m = f / kTile, row = f % kTile / kChunk, k = r0 + f % kChunk;
-        if (k >= p.r32 || p0 + m >= n_pieces) continue;
-        const Piece& o = s_piece[p0 + m];
-        if (row >= o.len || o.rank == 0) continue;
-        const float sc = p.scale ? p.scale[o.adapter] : 1.f;
+      // sums over the blocks; scale v and split it into bf16 terms
+      for (int e = tid * 2; e < own * 64; e += kAdThreads * 2) {
+        const int t = rank * own + e / 64, k = e % 64;
+        if (t >= sg.len || r0 + k >= p.r32) continue;
         float v[2] = {0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < kAdCluster; ++c) {
-          const float2 w = *reinterpret_cast<const float2*>(slots + c * kSlot + e);
+        for (int c = 0; c < split; ++c) {
+          const float2 w = *reinterpret_cast<const float2*>(slots + c * own * 64 + e);
           v[0] += w.x, v[1] += w.y;
         }
-        v[0] *= sc, v[1] *= sc;
-        for (int t = 0; t < p.n_terms; ++t) {
-          uint16_t* d = vt + t * v_plane + (o.start + row) * p.v_ld + k;
-          *reinterpret_cast<uint32_t*>(d) = next_term(v);
-          if (kChunk == 16) *reinterpret_cast<uint32_t*>(d + 16) = 0;
-        }
+        v[0] = k < n_r ? v[0] * sc : 0.f;
+        v[1] = k + 1 < n_r ? v[1] * sc : 0.f;
+        for (int i = 0; i < p.n_terms; ++i)
+          *reinterpret_cast<uint32_t*>(vt + i * v_plane + (sg.start + t) * p.v_ld + r0 + k) =
+              next_term(v);
       }
-      // the sums have been read before the next step's arrive
-      cluster_arrive();
-      cluster_wait();
+      // relaxed: nothing is handed over (a release would wait for v's stores)
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      sums_read = true;
     }
   }
+  if (sums_read) cluster_wait();
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
+constexpr int kBlk = 128;          // rows (of W) of an expand step
+constexpr int kVTile = 64 * 128;   // bytes of 64 ranks of v
+constexpr int kBTile = 128 * 128;  // of B
+constexpr int kExpandStages = 3;
 
-constexpr int kBlk = 64;  // rows (of W) of an expand step
-
-// y = base + B v over (64 tokens) x (tile_rows rows) tiles.  Per step (one
-// segment of the tile, 64 rows) base [64][64] and B [64][rank] are copied to
-// shared memory asynchronously, STAGES - 1 steps ahead.  Warp w multiplies
-// tokens 16 (w % 4) .. + 15 with rows 32 (w / 4) .. + 31.  Within both operands
-// a lane holds 8 consecutive ranks of each 32 (two MMA steps).  Shared-memory
-// rows are a multiple of 128 bytes or 64 apart; 16-byte pieces are swapped by
-// row so that 8 lanes of two (base fp32, B) or four (base bf16) rows take all
-// banks.
-// KS: 32-rank steps, v's fragments stay in registers; 0: any number, from
-// shared memory.
-template <int KS, bool F32, bool VEC, int STAGES>
-__global__ void __launch_bounds__(kAdThreads, KS ? 2 : 1) expand_kernel(const AdapterParams p) {
-  constexpr int kTerms = F32 ? 3 : 2;
-  constexpr int kES = F32 ? 4 : 2;  // bytes of an element of y
-  constexpr int kRow = kBlk * kES, kPieces = kRow / 16;
-  constexpr int kRowsAt = kAdThreads / kPieces;  // tile rows a pass of the block copies
-  constexpr int kPasses = kTileTokens / kRowsAt;
-  constexpr int kBase = kTileTokens * kRow;      // bytes of a stage's base
+// y = base + B v over (64 tokens) x (tile_rows rows) tiles, 128 rows at a time
+// for each segment of the tile: D[row][token] = B [128][rank] x v^T [rank][64]
+// on tcgen05, one product per bf16 term of v into the same accumulator.  The
+// product is taken this way round because tensor memory hands each lane one row
+// of D: a warp's 32 lanes then hold 32 neighbouring rows of W for a token, and
+// base and y move in whole 128-byte lines at any alignment.  B is copied to
+// shared memory asynchronously in steps of 64 ranks, STAGES - 1 steps ahead;
+// base is loaded 128 rows ahead into registers.
+// NC: 64-rank steps at most.  VEC: 16-byte copies of B are legal.
+template <int NC, bool F32, bool VEC>
+__global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(const AdapterParams p) {
+  constexpr int STAGES = kExpandStages, kTerms = F32 ? 3 : 2;
   using E = typename std::conditional<F32, float, uint16_t>::type;
-  extern __shared__ __align__(16) uint8_t smem[];  // stages
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ TileInfo s_info;
+  __shared__ int64_t s_base[kTileTokens], s_y[kTileTokens];  // byte offsets of the segment's tokens
+  __shared__ __align__(8) uint64_t s_bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_gave_up;
+  const uint32_t sm = (smem_u32(smem) + 1023) & ~1023u;  // v: [term][step], then the stages of B
+  uint8_t* const smp = smem + (sm - smem_u32(smem));
+  const uint32_t st0 = kTerms * NC * kVTile;             // offset of the stages
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, q = lane & 3, mp = warp & 3, half = warp >> 2;
-  const int v_plane = kTileTokens * p.v_ld;
-  const int r32 = KS ? 32 * KS : p.r32;
-  const int b_row = 2 * r32, b_pieces = r32 / 8;  // bytes, 16-byte pieces of a row of B
-  const int b_swap = b_row % 128 == 0 ? 4 : 0;
-  const int stage_bytes = kBase + kBlk * b_row;
   const int n_chunks = (p.rows + p.tile_rows - 1) / p.tile_rows;
   const int64_t tile = blockIdx.x / n_chunks;
   const int first = blockIdx.x % n_chunks * p.tile_rows;  // the block's rows
   const int rows = min(p.rows - first, p.tile_rows), nb = (rows + kBlk - 1) / kBlk;
-  const E* base = static_cast<const E*>(p.base);
   const bool in_place = p.base == p.y;
   const uint8_t* ws = p.ws + tile * tile_bytes(kTerms, p.v_ld);
   const uint16_t* vt = reinterpret_cast<const uint16_t*>(ws + sizeof(TileInfo));
+  const uint32_t bar = smem_u32(&s_bar);
   pdl_wait();
+  if (tid == 0) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_gave_up = 0;
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s_tmem)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
   if (tid < static_cast<int>(sizeof(TileInfo) / 16))
     reinterpret_cast<uint4*>(&s_info)[tid] = reinterpret_cast<const uint4*>(ws)[tid];
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
   const int n_segments = s_info.n_segments;
 
-  // The copies run ahead, with their own place.  A thread copies one 16-byte
-  // piece of every kRowsAt-th row of base and of every few rows of B.
-  int l_seg = 0, l_blk = 0, l_stage = 0;
-  Piece l_sg;
-  const E* l_base[kPasses];
-  const uint16_t* l_b = nullptr;
-  int l_bytes = 0;  // of the thread's piece of B, inside the rank
-  const int row_a = tid / kPieces, pc_a = tid % kPieces;
-  const int row_b = tid / b_pieces, pc_b = tid % b_pieces;
-  const int b_step = kAdThreads / b_pieces;  // rows a pass copies (b_pieces divides 256 if KS)
-  const uint32_t dst_a = smem_u32(smem) + row_a * kRow +
-                         (F32 ? pc_a ^ (row_a & 1) << 2 : pc_a ^ (row_a & 3) << 1) * 16;
-  const uint32_t dst_b = smem_u32(smem) + kBase + row_b * b_row + (pc_b ^ (row_b & 1) * b_swap) * 16;
-  auto open_segment = [&]() {
-    l_sg = s_info.segment[l_seg];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int r = min(row_a + i * kRowsAt, l_sg.len - 1);
-      l_base[i] = base + s_info.tok[l_sg.start + r] * p.base_ld + first + pc_a * (16 / kES);
-    }
-    l_b = p.b + (static_cast<int64_t>(max(l_sg.adapter, 0)) * p.rows + first) * p.r_max;
-    l_bytes = min(max(2 * (l_sg.rank - 8 * pc_b), 0), 16);
-    if (VEC && KS) l_b += static_cast<int64_t>(row_b) * p.r_max + pc_b * 8;
-  };
+  // The copies of B run ahead, with their own place: one 16-byte piece of
+  // every 32nd row.
+  int l_seg = 0, l_blk = 0, l_step = 0, l_stage = 0;
+  const int l_pc = tid & 7;
+  const int64_t l_at = static_cast<int64_t>(tid >> 3) * p.r_max + 8 * l_pc;
+  const uint32_t l_off = operand_off(tid >> 3, l_pc);
   auto issue = [&]() {
     if (l_seg < n_segments) {
-      if (l_blk == 0) open_segment();
-      const int left = rows - l_blk * kBlk;  // rows of W from this step on
-      const uint32_t at = l_stage * stage_bytes;
-      if (l_sg.rank > 0 || !in_place) {
-        if (p.base) {
-          if constexpr (VEC) {
-            const int bytes = pc_a * (16 / kES) < left ? 16 : 0;
+      const Piece sg = s_info.segment[l_seg];
+      const int left = rows - l_blk * kBlk;  // rows of W from this block on
+      const int rank = sg.rank - l_step * 64;
+      const int pieces = min((rank + 15) / 16 * 2, 8);  // 16-byte pieces of whole MMA steps
+      const uint16_t* b = p.b + (static_cast<int64_t>(max(sg.adapter, 0)) * p.rows + first +
+                                 l_blk * kBlk) * p.r_max + l_step * 64;
+      const uint32_t dst = st0 + l_stage * kBTile;
+      if constexpr (VEC) {
+        const int bytes = min(max(2 * (rank - 8 * l_pc), 0), 16);
+        const int rows_in = min(left - (tid >> 3), kBlk);  // every 32nd of them
+        const uint16_t* src = b + l_at;
+        if (l_pc < pieces)
 #pragma unroll
-            for (int i = 0; i < kPasses; ++i)
-              if (row_a + i * kRowsAt < l_sg.len)
-                cp_async16(dst_a + at + i * kRowsAt * kRow, bytes ? l_base[i] + l_blk * kBlk : base,
-                           bytes);
-          } else {
+          for (int i = 0; i < 4; ++i) {
+            const int n = 32 * i < rows_in ? bytes : 0;
+            cp_async16(sm + dst + l_off + i * 4096, n ? src + i * 32ll * p.r_max : p.b, n);
+          }
+      } else if (pieces > 0) {
 #pragma unroll 4
-            for (int i = tid; i < l_sg.len * kBlk; i += kAdThreads) {
-              const int row = i / kBlk, c = i % kBlk, pc = c * kES / 16;
-              const int sw = F32 ? pc ^ (row & 1) << 2 : pc ^ (row & 3) << 1;
-              E v = E(0);
-              if (c < left)
-                v = (base + s_info.tok[l_sg.start + row] * p.base_ld)[first + l_blk * kBlk + c];
-              *reinterpret_cast<E*>(smem + at + row * kRow + sw * 16 + c * kES % 16) = v;
-            }
-          }
-        }
-        const uint16_t* b = l_b + static_cast<int64_t>(l_blk * kBlk) * p.r_max;
-        if constexpr (VEC && KS) {
-#pragma unroll
-          for (int i = 0; i < kBlk * 4 * KS / kAdThreads; ++i) {
-            const int bytes = row_b + i * b_step < left ? l_bytes : 0;
-            cp_async16(dst_b + at + i * b_step * b_row, bytes ? b + i * b_step * p.r_max : p.b, bytes);
-          }
-        } else if constexpr (VEC) {
-          for (int i = tid; i < kBlk * b_pieces; i += kAdThreads) {
-            const int row = i / b_pieces, pc = i % b_pieces;
-            const int bytes = row < left ? min(max(2 * (l_sg.rank - 8 * pc), 0), 16) : 0;
-            cp_async16(smem_u32(smem) + at + kBase + row * b_row + (pc ^ (row & 1) * b_swap) * 16,
-                       bytes ? b + static_cast<int64_t>(row) * p.r_max + pc * 8 : p.b, bytes);
-          }
-        } else {
-#pragma unroll 4
-          for (int i = tid; i < kBlk * r32; i += kAdThreads) {
-            const int row = i / r32, k = i % r32;
-            uint16_t v = 0;
-            if (k < l_sg.rank && row < left) v = b[static_cast<int64_t>(row) * p.r_max + k];
-            *reinterpret_cast<uint16_t*>(smem + at + kBase + row * b_row +
-                                         (k / 8 ^ (row & 1) * b_swap) * 16 + k % 8 * 2) = v;
-          }
+        for (int i = tid; i < kBlk * pieces * 8; i += kAdThreads) {
+          const int row = i / (pieces * 8), k = i % (pieces * 8);
+          uint16_t v = 0;
+          if (k < rank && row < left) v = b[static_cast<int64_t>(row) * p.r_max + k];
+          *reinterpret_cast<uint16_t*>(smp + dst + operand_off(row, k >> 3) + (k & 7) * 2) = v;
         }
       }
       l_stage = l_stage + 1 == STAGES ? 0 : l_stage + 1;
-      if (++l_blk == nb) l_blk = 0, ++l_seg;
+      if (NC > 1 && (l_step + 1) * 64 < sg.rank) {
+        ++l_step;
+      } else {
+        l_step = 0;
+        if (++l_blk == nb) l_blk = 0, ++l_seg;
+      }
     }
+    __syncwarp();
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) issue();
 
-  // this lane's places within a stage
-  const int m0 = mp * 16, col = half * 32 + 4 * q;
-  const uint8_t* at_b = smem + kBase + (half * 32 + 4 * (g >> 1) + (g & 1)) * b_row;
-  const uint8_t* at_base[2];  // row m0 + g, row halves; row m0 + g + 8 is 8 kRow behind
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int at = (col + 16 * w) * kES, pc = at / 16;
-    at_base[w] = smem + (m0 + g) * kRow + (F32 ? pc ^ (g & 1) << 2 : pc ^ (g & 3) << 1) * 16 + at % 16;
-  }
+  // This thread's row within a block of 128, and its 32 tokens of the segment.
+  const int my_row = (warp & 3) * 32 + lane, n0 = (warp >> 2) * 32;
+  const uint32_t t_addr = tmem + (static_cast<uint32_t>(warp & 3) * 32 << 16) + n0;
   int stage = 0;
+  uint32_t phase = 0;
   for (int seg = 0; seg < n_segments; ++seg) {
     const Piece sg = s_info.segment[seg];
-    const int n_k = (sg.rank + 31) / 32;
-    const bool work = m0 < sg.len && (sg.rank > 0 || !in_place);
-    // rows behind the segment's last stand for nothing and are not stored
-    const uint16_t* v0 = vt + min(sg.start + m0 + g, kTileTokens - 1) * p.v_ld + 8 * q;
-    const uint16_t* v1 = vt + min(sg.start + m0 + g + 8, kTileTokens - 1) * p.v_ld + 8 * q;
-    uint4 vf[KS ? KS : 1][kTerms][2];  // v's fragments of the segment
-    if (KS && work) {
+    const bool write = sg.rank > 0 || !in_place;
+    // v's rows and the tokens' offsets; every thread is past the last
+    // segment's products and rows
+    __syncthreads();
+    const int pieces = (sg.rank + 15) / 16 * 2;
+    if (tid >> 2 < sg.len) {  // four threads a row
+      const int row = tid >> 2;
+      const uint16_t* src = vt + (sg.start + row) * p.v_ld + 8 * (tid & 3);
+      for (int c = 0; c < NC && 8 * c < pieces; ++c) {
+        uint4 v[kTerms][2];
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
-        if (k < n_k)
+        for (int t = 0; t < kTerms; ++t)
 #pragma unroll
-          for (int t = 0; t < kTerms; ++t) {
-            vf[k][t][0] = *reinterpret_cast<const uint4*>(v0 + t * v_plane + 32 * k);
-            vf[k][t][1] = *reinterpret_cast<const uint4*>(v1 + t * v_plane + 32 * k);
-          }
+          for (int i = 0; i < 2; ++i)
+            if (8 * c + (tid & 3) + 4 * i < pieces)
+              v[t][i] = *reinterpret_cast<const uint4*>(src + t * kTileTokens * p.v_ld + 64 * c + 32 * i);
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (8 * c + (tid & 3) + 4 * i < pieces)
+              *reinterpret_cast<uint4*>(smp + (t * NC + c) * kVTile +
+                                        operand_off(row, (tid & 3) + 4 * i)) = v[t][i];
+      }
     }
-    E* y[2];
+    if (tid < sg.len) {
+      s_base[tid] = s_info.tok[sg.start + tid] * p.base_ld * static_cast<int64_t>(sizeof(E));
+      s_y[tid] = s_info.tok[sg.start + tid] * p.y_ld * static_cast<int64_t>(sizeof(E));
+    }
+    __syncthreads();
+    const int n_tok = min(max(sg.len - n0, 0), 32);
+    // 32 whole neighbours (a segment's tokens ascend): their rows are one stride apart
+    const bool run = n_tok == 32 && s_info.tok[sg.start + n0 + 31] - s_info.tok[sg.start + n0] == 31;
+    const int64_t base_step = p.base_ld * static_cast<int64_t>(sizeof(E)),
+                  y_step = p.y_ld * static_cast<int64_t>(sizeof(E));
+    const uint32_t idesc = mma_idesc((sg.len + 15) / 16 * 16);
+    E add[32];  // base of this thread's row
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(static_cast<const E*>(p.base) + first + my_row);
+    uint8_t* y = reinterpret_cast<uint8_t*>(static_cast<E*>(p.y) + first + my_row);
+    auto load_base = [&](int blk) {
+      if (!p.base || !write || blk * kBlk + my_row >= rows) return;
+      const uint8_t* src = base + blk * kBlk * static_cast<int>(sizeof(E));
+      if (run) {
+        src += s_base[n0];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      y[h] = static_cast<E*>(p.y) +
-             s_info.tok[min(sg.start + m0 + g + 8 * h, sg.start + sg.len - 1)] * p.y_ld + first + col;
-    for (int blk = 0; blk < nb; ++blk) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-      __syncthreads();  // this step's data is there; the last step's has been read
-      issue();
-      const int at = stage * stage_bytes;
-      stage = stage + 1 == STAGES ? 0 : stage + 1;
-      if (!work) continue;
-      // MMA column g of tile j is row 16 (j / 2) + 4 (g / 2) + 2 (j % 2) + g % 2
-      const uint8_t* bp = at_b + at;
-      float acc[4][4] = {};
-      auto step = [&](int k, const uint4(&f)[kTerms][2]) {
-        const int pc = (4 * k + q) ^ (g & 1) * b_swap;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 w =
-              *reinterpret_cast<const uint4*>(bp + (16 * (j >> 1) + 2 * (j & 1)) * b_row + pc * 16);
-#pragma unroll
-          for (int t = 0; t < kTerms; ++t) {
-            mma16816(acc[j], f[t][0].x, f[t][1].x, f[t][0].y, f[t][1].y, w.x, w.y);
-            mma16816(acc[j], f[t][0].z, f[t][1].z, f[t][0].w, f[t][1].w, w.z, w.w);
-          }
-        }
-      };
-      if constexpr (KS > 0) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-          if (k < n_k) step(k, vf[k]);
+        for (int j = 0; j < 32; ++j, src += base_step) add[j] = *reinterpret_cast<const E*>(src);
       } else {
-        for (int k = 0; k < n_k; ++k) {
 #pragma unroll
-          for (int t = 0; t < kTerms; ++t) {
-            vf[0][t][0] = *reinterpret_cast<const uint4*>(v0 + t * v_plane + 32 * k);
-            vf[0][t][1] = *reinterpret_cast<const uint4*>(v1 + t * v_plane + 32 * k);
+        for (int j = 0; j < 32; ++j)
+          if (j < n_tok) add[j] = *reinterpret_cast<const E*>(src + s_base[n0 + j]);
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < 32; ++j) add[j] = E(0);
+    load_base(0);
+    for (int blk = 0; blk < nb; ++blk) {
+      for (int r0 = 0; r0 == 0 || (NC > 1 && r0 < sg.rank); r0 += 64) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();  // this step's B is there, the accumulator has been read
+        const int n_k = min((sg.rank - r0 + 15) / 16, 4);  // MMA steps of a term
+        if (warp == 0 && n_k > 0) {
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t b = operand_desc(sm + st0 + stage * kBTile);
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t) {
+              const uint64_t v = operand_desc(sm + (t * NC + (r0 >> 6)) * kVTile);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k < n_k) tc_mma(tmem, b + 2 * k, v + 2 * k, idesc, (NC > 1 ? r0 : 0) | t | k);
+            }
+            asm volatile(
+                "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                    bar)
+                : "memory");
           }
-          step(k, vf[0]);
+          __syncwarp();
+        }
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        issue();  // into the stage of the step before, whose products are done
+        if (n_k > 0) {
+          mbar_wait(bar, phase, &s_gave_up);
+          phase ^= 1;
         }
       }
-      const int left = rows - blk * kBlk - col;
+      float v[32];
+      if (sg.rank > 0 && n_tok > 0) {  // the same for the warp
+        tc_fence_after();
+        tmem_ld32(t_addr, v);
+        tc_fence_before();
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (m0 + g + 8 * h >= sg.len) continue;
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+      }
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (left <= 16 * w) continue;
-          float v[4] = {};
-          if (p.base) {
-            const uint8_t* src = at_base[w] + at + 8 * h * kRow;
-            if constexpr (F32) {
-              const float4 b = *reinterpret_cast<const float4*>(src);
-              v[0] = b.x, v[1] = b.y, v[2] = b.z, v[3] = b.w;
-            } else {
-              const uint2 b = *reinterpret_cast<const uint2*>(src);
-              v[0] = __uint_as_float(b.x << 16), v[1] = __uint_as_float(b.x & 0xffff0000u);
-              v[2] = __uint_as_float(b.y << 16), v[3] = __uint_as_float(b.y & 0xffff0000u);
-            }
-          }
+      for (int j = 0; j < 32; ++j) {
+        if constexpr (F32)
+          v[j] += add[j];
+        else
+          v[j] += bf16_value(add[j]);
+      }
+      if (blk + 1 < nb) load_base(blk + 1);
+      if (write && blk * kBlk + my_row < rows) {
+        uint8_t* dst = y + blk * kBlk * static_cast<int>(sizeof(E));
+        auto put = [&](uint8_t* at, float f) {
+          if constexpr (F32)
+            *reinterpret_cast<float*>(at) = f;
+          else
+            *reinterpret_cast<uint16_t*>(at) = bf16_bits(f);
+        };
+        if (run) {
+          dst += s_y[n0];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += acc[2 * w + (i >> 1)][2 * h + (i & 1)];
-          E* dst = y[h] + blk * kBlk + 16 * w;
-          if constexpr (VEC) {
-            if constexpr (F32)
-              *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-            else
-              *reinterpret_cast<uint2*>(dst) =
-                  make_uint2(bf16_bits(v[0]) | static_cast<uint32_t>(bf16_bits(v[1])) << 16,
-                             bf16_bits(v[2]) | static_cast<uint32_t>(bf16_bits(v[3])) << 16);
-          } else {
+          for (int j = 0; j < 32; ++j, dst += y_step) put(dst, v[j]);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (i < left - 16 * w) {
-                if constexpr (F32)
-                  dst[i] = v[i];
-                else
-                  dst[i] = bf16_bits(v[i]);
-              }
-          }
+          for (int j = 0; j < 32; ++j)
+            if (j < n_tok) put(dst + s_y[n0 + j], v[j]);
         }
       }
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
 // ---- host ------------------------------------------------------------------
@@ -996,52 +1158,50 @@ int v_stride(int max_rank) {
   return r32 % 64 == 0 ? r32 + 32 : r32;
 }
 
+// Few tokens: one launch.
 template <int NT, bool MULTI, bool F32, bool VEC>
-cudaError_t launch_shape(AdapterParams p, int n_sm, cudaStream_t s) {
+cudaError_t launch_few(AdapterParams p, cudaStream_t s) {
   constexpr int kTile = 16 * 8 * NT;
-  cudaError_t e;
-  if (p.T <= kNarrow) {
-    // a window holds at most one piece per 16 tokens and one more per adapter
-    // or none at all
-    const int64_t most = static_cast<int64_t>(p.n) + 1 + kWindow / 16;
-    p.per_window = static_cast<int>(most < kWindow ? most : kWindow);
-    const int full = p.T / kWindow, rest = p.T % kWindow;
-    const int64_t last = static_cast<int64_t>(p.n) + 1 + rest / 16;
-    const int64_t clusters = static_cast<int64_t>(full) * p.per_window +
-                             (last < rest ? last : rest);
-    const size_t smem = sizeof(float) * kTile * (kAdWarps + (MULTI ? 2 : 1) * kAdCluster) +
-                        sizeof(uint16_t) * p.n_terms * 16 * p.v_ld;
-    e = allow_smem<adapter_kernel<NT, MULTI, F32, VEC>>(smem);
-    if (e != cudaSuccess) return e;
-    return launch(adapter_kernel<NT, MULTI, F32, VEC>, clusters * kAdCluster, kAdCluster, smem, s, p);
-  }
-  const int64_t tiles = (static_cast<int64_t>(p.T) + kTileTokens - 1) / kTileTokens;
-  const size_t sums = sizeof(float) * kTile * (kAdWarps + 4);
-  e = allow_smem<shrink_kernel<NT, VEC>>(sums);
+  // a window holds at most one piece per 16 tokens and one more per adapter
+  // or none at all
+  const int64_t most = static_cast<int64_t>(p.n) + 1 + kWindow / 16;
+  p.per_window = static_cast<int>(most < kWindow ? most : kWindow);
+  const int full = p.T / kWindow, rest = p.T % kWindow;
+  const int64_t last = static_cast<int64_t>(p.n) + 1 + rest / 16;
+  const int64_t clusters = static_cast<int64_t>(full) * p.per_window + (last < rest ? last : rest);
+  const size_t smem = sizeof(float) * kTile * (kAdWarps + (MULTI ? 2 : 1) * kAdCluster) +
+                      sizeof(uint16_t) * p.n_terms * 16 * p.v_ld;
+  const cudaError_t e = allow_smem<adapter_kernel<NT, MULTI, F32, VEC>>(smem);
   if (e != cudaSuccess) return e;
-  e = launch(shrink_kernel<NT, VEC>, tiles * kAdCluster, kAdCluster, sums, s, p);
-  if (e != cudaSuccess) return e;
-  // two blocks an SM up to rank 64
-  constexpr int kSteps = MULTI ? 0 : NT == 8 ? 2 : 1, kStages = MULTI ? 3 : 4;
-  const size_t smem = kStages * (kTileTokens * kBlk * (F32 ? 4 : 2) +
-                                 kBlk * 2 * (kSteps ? 32 * kSteps : p.r32));
-  e = allow_smem<expand_kernel<kSteps, F32, VEC, kStages>>(smem);
-  if (e != cudaSuccess) return e;
-  // narrower tiles while they do not fill the GPU
-  p.tile_rows = 512;
-  while (p.tile_rows > kBlk && tiles * ((p.rows + p.tile_rows - 1) / p.tile_rows) < 4 * n_sm)
-    p.tile_rows /= 2;
-  const int64_t blocks = tiles * ((p.rows + p.tile_rows - 1) / p.tile_rows);
-  if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  return launch(expand_kernel<kSteps, F32, VEC, kStages>, blocks, 1, smem, s, p);
+  return launch(adapter_kernel<NT, MULTI, F32, VEC>, clusters * kAdCluster, kAdCluster, smem, s, p);
+}
+template <bool F32, bool VEC>
+cudaError_t launch_few(const AdapterParams& p, cudaStream_t s) {
+  if (p.r_max <= 16) return launch_few<2, false, F32, VEC>(p, s);
+  if (p.r_max <= 32) return launch_few<4, false, F32, VEC>(p, s);
+  if (p.r_max <= 64) return launch_few<8, false, F32, VEC>(p, s);
+  return launch_few<8, true, F32, VEC>(p, s);
 }
 
+// Many: two.
+template <bool VEC>
+cudaError_t launch_shrink(const AdapterParams& p, int64_t tiles, cudaStream_t s) {
+  const size_t smem = 1024 + kShrinkStages * kShrinkStage;
+  const cudaError_t e = allow_smem<shrink_kernel<VEC>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch(shrink_kernel<VEC>, tiles * p.split, p.split, smem, s, p);
+}
+template <int NC, bool F32, bool VEC>
+cudaError_t launch_expand(const AdapterParams& p, int64_t blocks, cudaStream_t s) {
+  const size_t smem = 1024 + NC * (F32 ? 3 : 2) * kVTile + kExpandStages * kBTile;
+  const cudaError_t e = allow_smem<expand_kernel<NC, F32, VEC>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch(expand_kernel<NC, F32, VEC>, blocks, 1, smem, s, p);
+}
 template <bool F32, bool VEC>
-cudaError_t launch_rank(const AdapterParams& p, int n_sm, cudaStream_t s) {
-  if (p.r_max <= 16) return launch_shape<2, false, F32, VEC>(p, n_sm, s);
-  if (p.r_max <= 32) return launch_shape<4, false, F32, VEC>(p, n_sm, s);
-  if (p.r_max <= 64) return launch_shape<8, false, F32, VEC>(p, n_sm, s);
-  return launch_shape<8, true, F32, VEC>(p, n_sm, s);
+cudaError_t launch_expand(const AdapterParams& p, int64_t blocks, cudaStream_t s) {
+  return p.r_max <= 64 ? launch_expand<1, F32, VEC>(p, blocks, s)
+                       : launch_expand<4, F32, VEC>(p, blocks, s);
 }
 
 bool aligned_to(const void* p, uintptr_t bytes) {
@@ -1109,12 +1269,13 @@ extern "C" pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const 
   p.T = T;
   p.cols = cols;
   p.rows = rows;
-  // every row of every matrix 16-byte aligned and a multiple of 16 bytes
+  // rows that are 16-byte aligned and whole 16-byte pieces: of x and A, of B,
+  // of base and y
   const int64_t per16 = 16 / static_cast<int64_t>(size);
-  const bool vec = cols % 8 == 0 && x_stride % 8 == 0 && aligned_to(d_x, 16) && aligned_to(d_a, 16) &&
-                   max_rank % 8 == 0 && aligned_to(d_b, 16) && rows % per16 == 0 &&
-                   y_stride % per16 == 0 && aligned_to(d_y, 16) &&
-                   (!d_base || (base_stride % per16 == 0 && aligned_to(d_base, 16)));
+  const bool vec_x = cols % 8 == 0 && x_stride % 8 == 0 && aligned_to(d_x, 16) && aligned_to(d_a, 16);
+  const bool vec_b = max_rank % 8 == 0 && aligned_to(d_b, 16);
+  const bool vec_y = rows % per16 == 0 && y_stride % per16 == 0 && aligned_to(d_y, 16) &&
+                     (!d_base || (base_stride % per16 == 0 && aligned_to(d_base, 16)));
   p.v_ld = v_stride(max_rank);
   p.r32 = (max_rank + 31) / 32 * 32;
   p.n_terms = y_type == PW_F32 ? 3 : 2;
@@ -1123,9 +1284,29 @@ extern "C" pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const 
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return record_error(PW_ERR_CUDA, cudaGetErrorString(e));
-  e = y_type == PW_F32
-                            ? (vec ? launch_rank<true, true>(p, n_sm, s) : launch_rank<true, false>(p, n_sm, s))
-                            : (vec ? launch_rank<false, true>(p, n_sm, s) : launch_rank<false, false>(p, n_sm, s));
+  const bool f32 = y_type == PW_F32;
+  // expand tiles: narrower while they do not fill the GPU
+  const int64_t tiles = (static_cast<int64_t>(T) + kTileTokens - 1) / kTileTokens;
+  p.tile_rows = 1024;
+  auto blocks_of = [&] { return tiles * ((rows + p.tile_rows - 1) / p.tile_rows); };
+  while (p.tile_rows > kBlk && blocks_of() * 2 < 3 * n_sm) p.tile_rows /= 2;
+  const int64_t blocks = blocks_of();
+  if (T > kNarrow && blocks >= (1ll << 31))
+    return record_error(PW_ERR_UNSUPPORTED, "pw_adapters: T * rows too large for one launch");
+  if (T <= kNarrow) {
+    const bool vec = vec_x && vec_b && vec_y;
+    e = f32 ? (vec ? launch_few<true, true>(p, s) : launch_few<true, false>(p, s))
+            : (vec ? launch_few<false, true>(p, s) : launch_few<false, false>(p, s));
+  } else {
+    // columns split while the blocks fit the GPU twice over
+    p.split = kAdCluster;
+    while (p.split > 1 && tiles * p.split > 2 * n_sm) p.split /= 2;
+    e = vec_x ? launch_shrink<true>(p, tiles, s) : launch_shrink<false>(p, tiles, s);
+    if (e != cudaSuccess) return record_error(PW_ERR_CUDA, cudaGetErrorString(e));
+    e = f32 ? (vec_b ? launch_expand<true, true>(p, blocks, s) : launch_expand<true, false>(p, blocks, s))
+            : (vec_b ? launch_expand<false, true>(p, blocks, s)
+                     : launch_expand<false, false>(p, blocks, s));
+  }
   if (e != cudaSuccess) return record_error(PW_ERR_CUDA, cudaGetErrorString(e));
   return PW_OK;
 }
