@@ -41,7 +41,7 @@ constexpr int kAdThreads = 256;
 constexpr int kAdWarps = kAdThreads / 32;
 constexpr int kAdCluster = 8;
 constexpr int kWindow = 256;     // tokens ordered together
-constexpr int kNarrow = 512;     // most tokens of the one-launch path
+constexpr int kNarrow = 1024;    // most tokens of the one-launch path
 constexpr int kTileTokens = 64;  // many tokens: tokens of a shrink cluster, of an expand tile
 constexpr int kMaxDevices = 64;
 
@@ -645,6 +645,18 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 constexpr int kShrinkStages = 5;
 constexpr int kShrinkStage = 2 * 64 * 128;  // bytes: x [64][64], A [64][64]
 constexpr int kTmemCols = 64;               // an accumulator
@@ -875,15 +887,20 @@ constexpr int kVTile = 64 * 128;   // bytes of 64 ranks of v
 constexpr int kBTile = 128 * 128;  // of B
 constexpr int kExpandStages = 3;
 
-// y = base + B v over (64 tokens) x (tile_rows rows) tiles, 128 rows at a time
-// for each segment of the tile: D[row][token] = B [128][rank] x v^T [rank][64]
-// on tcgen05, one product per bf16 term of v into the same accumulator.  The
-// product is taken this way round because tensor memory hands each lane one row
-// of D: a warp's 32 lanes then hold 32 neighbouring rows of W for a token, and
-// base and y move in whole 128-byte lines at any alignment.  B is copied to
-// shared memory asynchronously in steps of 64 ranks, STAGES - 1 steps ahead;
-// base is loaded 128 rows ahead into registers.
+// y = base + B v over (64 tokens) x (tile_rows rows) tiles, 128 rows at a time:
+// D_s[row][token] = B_s [128][rank] x v^T [rank][64] on tcgen05 for each of up
+// to kGroup neighbouring segments s of the tile, one product per bf16 term of v
+// into the segment's accumulator; a token takes its own segment's column.  (A
+// tile on the border of two requests then reads and writes its tokens once, and
+// values of one adapter never meet another's tokens.)  The product is taken
+// this way round because tensor memory hands each lane one row of D: a warp's
+// 32 lanes then hold 32 neighbouring rows of W for a token, and base and y move
+// in whole 128-byte lines at any alignment.  B is copied to shared memory
+// asynchronously in steps of 64 ranks, STAGES - 1 steps ahead; base is loaded
+// 128 rows ahead into registers.
 // NC: 64-rank steps at most.  VEC: 16-byte copies of B are legal.
+constexpr int kGroup = 4;
+constexpr int kExpandCols = 64 * kGroup;
 template <int NC, bool F32, bool VEC>
 __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(const AdapterParams p) {
   constexpr int STAGES = kExpandStages, kTerms = F32 ? 3 : 2;
@@ -915,7 +932,7 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&s_tmem)),
-                 "r"(kTmemCols));
+                 "r"(kExpandCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid < static_cast<int>(sizeof(TileInfo) / 16))
@@ -927,8 +944,8 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
   const int n_segments = s_info.n_segments;
 
   // The copies of B run ahead, with their own place: one 16-byte piece of
-  // every 32nd row.
-  int l_seg = 0, l_blk = 0, l_step = 0, l_stage = 0;
+  // every 32nd row.  Order: groups, blocks of 128 rows, segments, 64 ranks.
+  int l_g0 = 0, l_seg = 0, l_blk = 0, l_step = 0, l_stage = 0;
   const int l_pc = tid & 7;
   const int64_t l_at = static_cast<int64_t>(tid >> 3) * p.r_max + 8 * l_pc;
   const uint32_t l_off = operand_off(tid >> 3, l_pc);
@@ -965,7 +982,12 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
         ++l_step;
       } else {
         l_step = 0;
-        if (++l_blk == nb) l_blk = 0, ++l_seg;
+        if (++l_seg == min(l_g0 + kGroup, n_segments)) {
+          if (++l_blk == nb)
+            l_blk = 0, l_g0 = l_seg;
+          else
+            l_seg = l_g0;
+        }
       }
     }
     __syncwarp();
@@ -974,21 +996,25 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) issue();
 
-  // This thread's row within a block of 128, and its 32 tokens of the segment.
+  // This thread's row within a block of 128, and its 32 tokens of the group.
   const int my_row = (warp & 3) * 32 + lane, n0 = (warp >> 2) * 32;
   const uint32_t t_addr = tmem + (static_cast<uint32_t>(warp & 3) * 32 << 16) + n0;
   int stage = 0;
   uint32_t phase = 0;
-  for (int seg = 0; seg < n_segments; ++seg) {
-    const Piece sg = s_info.segment[seg];
-    const bool write = sg.rank > 0 || !in_place;
-    // v's rows and the tokens' offsets; every thread is past the last
-    // segment's products and rows
+  for (int g0 = 0; g0 < n_segments; g0 += kGroup) {
+    const int g1 = min(g0 + kGroup, n_segments);
+    const int start = s_info.segment[g0].start;
+    const int len = s_info.segment[g1 - 1].start + s_info.segment[g1 - 1].len - start;
+    int r_all = 0;
+    for (int i = g0; i < g1; ++i) r_all = max(r_all, s_info.segment[i].rank);
+    const bool write = r_all > 0 || !in_place;
+    // v's rows and the tokens' offsets; every thread is past the last group's
+    // products and rows
     __syncthreads();
-    const int pieces = (sg.rank + 15) / 16 * 2;
-    if (tid >> 2 < sg.len) {  // four threads a row
+    const int pieces = (r_all + 15) / 16 * 2;
+    if (tid >> 2 < len) {  // four threads a row
       const int row = tid >> 2;
-      const uint16_t* src = vt + (sg.start + row) * p.v_ld + 8 * (tid & 3);
+      const uint16_t* src = vt + (start + row) * p.v_ld + 8 * (tid & 3);
       for (int c = 0; c < NC && 8 * c < pieces; ++c) {
         uint4 v[kTerms][2];
 #pragma unroll
@@ -1006,17 +1032,21 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
                                         operand_off(row, (tid & 3) + 4 * i)) = v[t][i];
       }
     }
-    if (tid < sg.len) {
-      s_base[tid] = s_info.tok[sg.start + tid] * p.base_ld * static_cast<int64_t>(sizeof(E));
-      s_y[tid] = s_info.tok[sg.start + tid] * p.y_ld * static_cast<int64_t>(sizeof(E));
+    if (tid < len) {
+      s_base[tid] = s_info.tok[start + tid] * p.base_ld * static_cast<int64_t>(sizeof(E));
+      s_y[tid] = s_info.tok[start + tid] * p.y_ld * static_cast<int64_t>(sizeof(E));
     }
     __syncthreads();
-    const int n_tok = min(max(sg.len - n0, 0), 32);
-    // 32 whole neighbours (a segment's tokens ascend): their rows are one stride apart
-    const bool run = n_tok == 32 && s_info.tok[sg.start + n0 + 31] - s_info.tok[sg.start + n0] == 31;
+    const int n_tok = min(max(len - n0, 0), 32);
+    // 32 whole neighbours: their rows are one stride apart
+    bool run = n_tok == 32;
+    if (run) {
+      const int t = s_info.tok[start + n0 + lane];
+      run = __all_sync(0xffffffffu, t == __shfl_sync(0xffffffffu, t, 0) + lane);
+    }
     const int64_t base_step = p.base_ld * static_cast<int64_t>(sizeof(E)),
                   y_step = p.y_ld * static_cast<int64_t>(sizeof(E));
-    const uint32_t idesc = mma_idesc((sg.len + 15) / 16 * 16);
+    const uint32_t idesc = mma_idesc((len + 15) / 16 * 16);
     E add[32];  // base of this thread's row
     const uint8_t* base = reinterpret_cast<const uint8_t*>(static_cast<const E*>(p.base) + first + my_row);
     uint8_t* y = reinterpret_cast<uint8_t*>(static_cast<E*>(p.y) + first + my_row);
@@ -1033,57 +1063,86 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
           if (j < n_tok) add[j] = *reinterpret_cast<const E*>(src + s_base[n0 + j]);
       }
     };
+    // the next block's base on its way to the L2 before its loads, a lane a token:
+    // one instruction asks for the warp's 32 lines, and no register waits for them
+    // (copying alone 113 -> 93 us at 4096 tokens x 14336 rows; two blocks ahead
+    // 90, three 100, five 116)
+    auto prefetch_base = [&](int blk) {
+      const int c = blk * kBlk + (warp & 3) * 32;
+      if (p.base && write && lane < n_tok && c < rows)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            reinterpret_cast<const uint8_t*>(static_cast<const E*>(p.base) + first + c) +
+            s_base[n0 + lane]));
+    };
 #pragma unroll
     for (int j = 0; j < 32; ++j) add[j] = E(0);
     load_base(0);
     for (int blk = 0; blk < nb; ++blk) {
-      for (int r0 = 0; r0 == 0 || (NC > 1 && r0 < sg.rank); r0 += 64) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncthreads();  // this step's B is there, the accumulator has been read
-        const int n_k = min((sg.rank - r0 + 15) / 16, 4);  // MMA steps of a term
-        if (warp == 0 && n_k > 0) {
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t b = operand_desc(sm + st0 + stage * kBTile);
+      prefetch_base(blk + 1);
+      for (int seg = g0; seg < g1; ++seg) {
+        const int rank = s_info.segment[seg].rank;
+        for (int r0 = 0; r0 == 0 || (NC > 1 && r0 < rank); r0 += 64) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncthreads();  // this step's B is there, the accumulators have been read
+          const int n_k = min((rank - r0 + 15) / 16, 4);  // MMA steps of a term
+          if (warp == 0 && n_k > 0) {
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t b = operand_desc(sm + st0 + stage * kBTile);
+              const uint32_t d = tmem + (seg - g0) * 64;
 #pragma unroll
-            for (int t = 0; t < kTerms; ++t) {
-              const uint64_t v = operand_desc(sm + (t * NC + (r0 >> 6)) * kVTile);
+              for (int t = 0; t < kTerms; ++t) {
+                const uint64_t v = operand_desc(sm + (t * NC + (r0 >> 6)) * kVTile);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (k < n_k) tc_mma(tmem, b + 2 * k, v + 2 * k, idesc, (NC > 1 ? r0 : 0) | t | k);
+                for (int k = 0; k < 4; ++k)
+                  if (k < n_k) tc_mma(d, b + 2 * k, v + 2 * k, idesc, (NC > 1 ? r0 : 0) | t | k);
+              }
+              asm volatile(
+                  "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                      bar)
+                  : "memory");
             }
-            asm volatile(
-                "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                    bar)
-                : "memory");
+            __syncwarp();
           }
-          __syncwarp();
-        }
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
-        issue();  // into the stage of the step before, whose products are done
-        if (n_k > 0) {
-          mbar_wait(bar, phase, &s_gave_up);
-          phase ^= 1;
+          stage = stage + 1 == STAGES ? 0 : stage + 1;
+          issue();  // into the stage of the step before, whose products are done
+          if (n_k > 0) {
+            mbar_wait(bar, phase, &s_gave_up);
+            phase ^= 1;
+          }
         }
       }
+      // base plus the token's own segment's column, 16 tokens at a time
       float v[32];
-      if (sg.rank > 0 && n_tok > 0) {  // the same for the warp
-        tc_fence_after();
-        tmem_ld32(t_addr, v);
-        tc_fence_before();
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.f;
-      }
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         if constexpr (F32)
-          v[j] += add[j];
+          v[j] = add[j];
         else
-          v[j] += bf16_value(add[j]);
+          v[j] = bf16_value(add[j]);
       }
       if (blk + 1 < nb) load_base(blk + 1);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        for (int seg = g0; seg < g1; ++seg) {  // the same for the warp
+          const int from = s_info.segment[seg].start - start - n0 - 16 * c;
+          const int to = from + s_info.segment[seg].len;
+          if (s_info.segment[seg].rank == 0 || from >= 16 || to <= 0) continue;
+          float d[16];
+          tmem_ld16(t_addr + (seg - g0) * 64 + 16 * c, d);
+          if (from <= 0 && to >= 16) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[16 * c + j] += d[j];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j >= from && j < to) v[16 * c + j] += d[j];
+          }
+        }
+      }
+      tc_fence_before();
       if (write && blk * kBlk + my_row < rows) {
         uint8_t* dst = y + blk * kBlk * static_cast<int>(sizeof(E));
         auto put = [&](uint8_t* at, float f) {
@@ -1109,7 +1168,7 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
   __syncthreads();
   tc_fence_after();
   if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kExpandCols));
 }
 
 // ---- host ------------------------------------------------------------------
@@ -1285,12 +1344,20 @@ extern "C" pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const 
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return record_error(PW_ERR_CUDA, cudaGetErrorString(e));
   const bool f32 = y_type == PW_F32;
-  // expand tiles: narrower while they do not fill the GPU
   const int64_t tiles = (static_cast<int64_t>(T) + kTileTokens - 1) / kTileTokens;
-  p.tile_rows = 1024;
-  auto blocks_of = [&] { return tiles * ((rows + p.tile_rows - 1) / p.tile_rows); };
-  while (p.tile_rows > kBlk && blocks_of() * 2 < 3 * n_sm) p.tile_rows /= 2;
-  const int64_t blocks = blocks_of();
+  const int n_blk = (rows + kBlk - 1) / kBlk;
+  // rows of an expand tile, in 128s: the fewest steps over the rounds of blocks
+  // the GPU takes (two blocks an SM, one above rank 64), a block's start
+  // counted as two steps
+  int64_t least = INT64_MAX;
+  const int64_t slots = (max_rank <= 64 ? 2 : 1) * n_sm;
+  for (int per = 1; per <= n_blk; ++per) {
+    const int64_t n = tiles * ((n_blk + per - 1) / per);
+    const int64_t steps = (n + slots - 1) / slots * (per + 2);
+    if (steps < least) least = steps, p.tile_rows = per * kBlk;
+    if (n <= slots) break;
+  }
+  const int64_t blocks = tiles * ((rows + p.tile_rows - 1) / p.tile_rows);
   if (T > kNarrow && blocks >= (1ll << 31))
     return record_error(PW_ERR_UNSUPPORTED, "pw_adapters: T * rows too large for one launch");
   if (T <= kNarrow) {

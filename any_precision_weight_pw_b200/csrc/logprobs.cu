@@ -11,11 +11,12 @@
 //
 // The n best come from the same pass.  Every thread also keeps its best
 // vector: (largest logit, first such vector).  The n-th largest of these over
-// the block is a bound that at least n logits reach, and a logit reaching it
-// can only lie with one of the n threads whose best vector does: only those
-// n threads' logits (n / 512 of the row) are read a second time.  Keys carry
-// the index below the logit, so all keys differ, ties fall to the lower index
-// and a row of equal logits costs no more than another.
+// the block's groups of 8 threads is a bound that at least n logits reach, and
+// a logit reaching it can only lie with a thread whose best vector does: only
+// those threads' logits (about n / 512 of the row) are read a second time.  The
+// few logits that reach the bound are put in order by counting, for each, the
+// larger ones.  Keys carry the index below the logit, so all keys differ and
+// ties fall to the lower index.
 //
 // Few rows are split over a cluster; the blocks' sums and lists meet in the
 // first block's shared memory in rank order, so results never depend on timing.
@@ -110,6 +111,32 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// two fp32 lanes, each correctly rounded
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // Keys order logits: larger first, then the lower index; 0 is below every key.
 // Adding +0 makes -0 equal +0; a NaN of either sign is above +inf.
 __device__ __forceinline__ int order_of(float z) {
@@ -128,44 +155,22 @@ __device__ __forceinline__ float key_logit(unsigned long long k) {
   return __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
 }
 
-// 32 keys over the lanes, largest in lane 0 (bitonic).
-__device__ __forceinline__ unsigned long long exchange(unsigned long long k, int j, bool keep_max) {
+constexpr int kGroups = kLpThreads / 8;  // groups of 8 threads
+constexpr int kMaxCand = 1024;
+
+__device__ __forceinline__ unsigned long long shfl_max(unsigned long long k, int j) {
   const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, j);
-  return (k > o) == keep_max ? k : o;
+  return k > o ? k : o;
 }
-__device__ __forceinline__ unsigned long long sort32(unsigned long long k) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-    for (int j = size >> 1; j > 0; j >>= 1)
-      k = exchange(k, j, ((lane & j) == 0) == ((lane & size) == 0));
-  return k;
-}
-// the 32 largest of two sorted lists, sorted
-__device__ __forceinline__ unsigned long long merge32(unsigned long long a, unsigned long long b) {
-  const int lane = threadIdx.x & 31;
-  const unsigned long long o = __shfl_xor_sync(0xffffffffu, b, 31);  // b reversed
-  unsigned long long k = a > o ? a : o;
-#pragma unroll
-  for (int j = 16; j > 0; j >>= 1) k = exchange(k, j, (lane & j) == 0);
-  return k;
-}
-// Merges the sorted lists of warps 0..n-1 (n a power of two) into warp 0's;
-// list: [n][32] shared.  Ends with a barrier; list[0..31] holds the result.
-__device__ __forceinline__ unsigned long long merge_warps(unsigned long long k, int n,
-                                                          unsigned long long* list) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (warp < n) list[warp * 32 + lane] = k;
-  for (int step = 1; step < n; step <<= 1) {
-    __syncthreads();
-    if (warp < n && warp % (2 * step) == 0) {
-      k = merge32(k, list[(warp + step) * 32 + lane]);
-      list[warp * 32 + lane] = k;
-    }
+// How many of keys[0..n) are larger (n even).
+__device__ __forceinline__ int larger(const unsigned long long* keys, int n, unsigned long long k) {
+  int r = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; i += 2) {
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(keys + i);
+    r += (o.x > k) + (o.y > k);
   }
-  __syncthreads();
-  return k;
+  return r;
 }
 
 struct Sums {
@@ -206,8 +211,12 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
   constexpr int N = LogitVec<ZT>::N;
   __shared__ Sums part[kLpWarps];
   __shared__ Sums slot_sums[kLpMaxCluster];
-  __shared__ unsigned long long list[TOP ? kLpWarps * 32 : 1];
-  __shared__ unsigned long long slot_keys[TOP ? kLpMaxCluster * 32 : 1];
+  __shared__ __align__(16) unsigned long long s_group[TOP ? kGroups : 2];  // groups' best, then lists
+  __shared__ __align__(16) unsigned long long s_list[TOP ? kLpMaxCluster * 32 : 2];
+  __shared__ __align__(16) unsigned long long s_cand[TOP ? kMaxCand : 2];
+  __shared__ uint16_t s_thread[TOP ? kLpThreads : 1];
+  __shared__ unsigned long long s_bound;
+  __shared__ int s_threads, s_cands;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_split = p.n_split;
   const int rank = n_split > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -246,6 +255,8 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
     }
   };
   if (has_head) absorb_one(tid);
+  // even and odd logits of a vector sum apart, two at a time
+  f2 s2 = pack2(a.s, 0.f), u2 = pack2(a.u, 0.f);
   for (int v = v0 + tid; v < v1; v += U * kLpThreads) {
     uint4 q[U];
 #pragma unroll
@@ -272,15 +283,33 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
         if (i < v1 && o > best) best = o, best_at = head + i * N;
       }
     }
-    a = rescaled(a, mx);
+    {
+      const float d = max_nan(a.r - mx, kFar), f = ex2(d * kLog2e);
+      const f2 f_2 = pack2(f, f);
+      u2 = mul2(fma2(s2, pack2(d, d), u2), f_2);
+      s2 = mul2(s2, f_2);
+      a.r = mx;
+    }
+    const f2 minus = pack2(-mx, -mx), scale = pack2(kLog2e, kLog2e);
 #pragma unroll
     for (int k = 0; k < U; ++k)
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float d = max_nan(x[k][j] - mx, kFar), e = ex2(d * kLog2e);
-        a.s += e;
-        a.u = fmaf(e, d, a.u);
+      for (int j = 0; j < N; j += 2) {
+        float d0, d1, t0, t1;
+        unpack2(add2(pack2(x[k][j], x[k][j + 1]), minus), d0, d1);
+        const f2 d = pack2(max_nan(d0, kFar), max_nan(d1, kFar));
+        unpack2(mul2(d, scale), t0, t1);
+        const f2 e = pack2(ex2(t0), ex2(t1));
+        s2 = add2(s2, e);
+        u2 = fma2(e, d, u2);
       }
+  }
+  {
+    float lo, hi;
+    unpack2(s2, lo, hi);
+    a.s = lo + hi;
+    unpack2(u2, lo, hi);
+    a.u = lo + hi;
   }
   if (has_tail) absorb_one(tail0 + tid);
 
@@ -289,44 +318,75 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
   unsigned long long mine = 0;  // warp 0: lane i holds the block's i-th best
   if (TOP) {
     const int n = p.n_top;
-    merge_warps(sort32(best == INT32_MIN ? 0ull : make_key(best, best_at)), kLpWarps, list);
-    const unsigned long long bound = list[n - 1];
+    const unsigned long long key = best == INT32_MIN ? 0ull : make_key(best, best_at);
+    const unsigned long long gk = shfl_max(shfl_max(shfl_max(key, 1), 2), 4);
+    if ((lane & 7) == 0) s_group[tid >> 3] = gk;
+    if (tid < 32) s_list[tid] = 0;
+    if (tid == 0) s_threads = s_cands = 0, s_bound = 0;
+    __syncthreads();
+    // the n-th best group's key (0 with fewer groups in use: every logit counts)
+    if (tid < kGroups && s_group[tid] != 0 && larger(s_group, kGroups, s_group[tid]) == n - 1)
+      s_bound = s_group[tid];
+    __syncthreads();
+    const unsigned long long bound = s_bound;
     // A logit reaches the bound if it is larger, or equal and not behind the
-    // bound's vector.  (A block with fewer than n threads in use: bound 0.)
+    // bound's vector.
     const uint32_t last = bound ? static_cast<uint32_t>(~(key_index(bound) + N - 1)) : 0u;
     const unsigned long long reach = (bound & 0xffffffff00000000ull) | last;
-    for (int j = warp; j < n; j += kLpWarps) {
-      const unsigned long long key = list[j];
-      if (key == 0) break;
-      // the thread whose best vector this is
-      const int at = key_index(key);
-      const int owner = at < head     ? at
-                        : at >= tail0 ? at - tail0
-                                      : ((at - head) / N - v0) % kLpThreads;
-      auto offer = [&](unsigned long long c) {  // one key a lane, 0 for none
-        if (c < reach) c = 0;
-        if (__any_sync(0xffffffffu, c > __shfl_sync(0xffffffffu, mine, n - 1)))
-          mine = merge32(mine, sort32(c));
-      };
-      unsigned long long c = 0;
-      if (lane == 0 && rank == 0 && owner < head)
-        c = make_key(order_of(LogitVec<ZT>::one(z, owner)), owner);
-      if (lane == 1 && rank == n_split - 1 && owner < p.V - tail0)
-        c = make_key(order_of(LogitVec<ZT>::one(z, tail0 + owner)), tail0 + owner);
-      offer(c);
-      for (int b = v0 + owner; b < v1; b += 32 * kLpThreads) {
-        const int64_t i = b + static_cast<int64_t>(lane) * kLpThreads;
-        float x[N];
-        if (i < v1) {
+    if (key != 0 && key >= bound) s_thread[atomicAdd(&s_threads, 1)] = static_cast<uint16_t>(tid);
+    __syncthreads();
+    // visit(key) for every logit of the listed threads, a warp a thread
+    const int n_threads = s_threads;
+    auto scan = [&](auto visit) {
+      for (int j = warp; j < n_threads; j += kLpWarps) {
+        const int owner = s_thread[j];
+        if (lane == 0 && rank == 0 && owner < head)
+          visit(make_key(order_of(LogitVec<ZT>::one(z, owner)), owner));
+        if (lane == 1 && rank == n_split - 1 && owner < p.V - tail0)
+          visit(make_key(order_of(LogitVec<ZT>::one(z, tail0 + owner)), tail0 + owner));
+        for (int64_t i = v0 + owner + static_cast<int64_t>(lane) * kLpThreads; i < v1;
+             i += 32 * kLpThreads) {
+          float x[N];
           LogitVec<ZT>::widen(zv[i], x);
-        }
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-          offer(i < v1 ? make_key(order_of(x[e]), head + static_cast<int>(i) * N + e) : 0ull);
+          for (int e = 0; e < N; ++e)
+            visit(make_key(order_of(x[e]), head + static_cast<int>(i) * N + e));
+        }
+      }
+    };
+    scan([&](unsigned long long k) {
+      if (k < reach) return;
+      const int at = atomicAdd(&s_cands, 1);
+      if (at < kMaxCand) s_cand[at] = k;
+    });
+    __syncthreads();
+    const int n_cand = s_cands;
+    if (n_cand <= kMaxCand) {  // the same order whatever order they came in
+      if (tid == 0 && (n_cand & 1)) s_cand[n_cand] = 0;  // kMaxCand is even
+      __syncthreads();
+      for (int i = tid; i < n_cand; i += kLpThreads) {
+        const int r = larger(s_cand, (n_cand + 1) & ~1, s_cand[i]);
+        if (r < n) s_list[r] = s_cand[i];
+      }
+    } else {  // many logits tie: one at a time
+      unsigned long long below = ~0ull;
+      for (int j = 0; j < n; ++j) {
+        unsigned long long top = 0;
+        scan([&](unsigned long long k) {
+          if (k < below && k > top) top = k;
+        });
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = shfl_max(top, o);
+        if (lane == 0) s_group[warp] = top;
+        __syncthreads();
+        below = 0;
+        for (int w = 0; w < kLpWarps; ++w) below = s_group[w] > below ? s_group[w] : below;
+        if (tid == 0) s_list[j] = below;
+        __syncthreads();
       }
     }
-    __syncthreads();  // every warp has read the bound and its threads
-    mine = merge_warps(mine, kLpWarps, list);
+    __syncthreads();
+    mine = s_list[lane];
   } else {
     __syncthreads();
   }
@@ -345,14 +405,23 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(d + 8), "f"(a.u) : "memory");
       }
       if (TOP) {
-        const uint32_t d = in_block0(&slot_keys[rank * 32 + lane]);
+        const uint32_t d = in_block0(&s_list[rank * 32 + lane]);
         asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(d), "l"(mine) : "memory");
       }
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank != 0) return;
-    if (TOP) mine = merge_warps(warp < n_split ? slot_keys[warp * 32 + lane] : 0ull, n_split, list);
+    if (TOP) {
+      if (tid < 32) s_group[tid] = 0;
+      __syncthreads();
+      if (tid < 32 * n_split && s_list[tid] != 0) {
+        const int r = larger(s_list, 32 * n_split, s_list[tid]);
+        if (r < p.n_top) s_group[r] = s_list[tid];
+      }
+      __syncthreads();
+      mine = s_group[lane];
+    }
     if (warp == 0) {
       a = lane < n_split ? slot_sums[lane] : Sums{-FLT_MAX, 0.f, 0.f};
       merge_lanes(a);

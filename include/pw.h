@@ -450,7 +450,7 @@ pw_status_t pw_token_logprobs(const void* d_logits, int32_t logits_type, int64_t
  * 16-byte pieces.  Accumulation is fp32, A_a x_t enters the second product
  * with 24 (y fp32) or 16 (y bf16) significant bits.  T >= 0,
  * 1 <= max_rank <= PW_MAX_ADAPTER_RANK.  d_workspace: device memory of
- * workspace_bytes >= pw_adapters_workspace_bytes (0 up to 512 tokens, then
+ * workspace_bytes >= pw_adapters_workspace_bytes (0 up to 1024 tokens, then
  * NULL is accepted), 16-byte aligned, used by this call alone until its work
  * is done; its contents need not be set or kept. */
 #define PW_MAX_ADAPTER_RANK 256

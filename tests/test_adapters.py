@@ -81,7 +81,7 @@ def check(gpu, d, **kw):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [1, 2, 17, 64, 255, 257, 512, 600, 2500])
+@pytest.mark.parametrize("T", [1, 2, 17, 64, 255, 257, 600, 1024, 1100, 2500])
 @pytest.mark.parametrize("order", ["mixed", "runs", "same"])
 @pytest.mark.parametrize("r,y", [(16, F32), (64, BF16), (5, F32), (72, F32)])
 def test_matches_float64(gpu, T, order, r, y):
@@ -271,8 +271,8 @@ OK = dict(x=4096, x_ld=64, a=8192, b=16384, ids=32768, ranks=33024, scale=33280,
     (dict(x=None), 1), (dict(a=None), 1), (dict(b=None), 1), (dict(ids=None), 1), (dict(y=None), 1),
     (dict(x_ld=-1), 1), (dict(y_ld=63), 1), (dict(base_ld=-1), 1), (dict(base=131072, base_ld=72), 1),
     (dict(x=4097), 1), (dict(a=8193), 1), (dict(ids=32770), 1), (dict(y=131074), 1),
-    (dict(T=513), 1), (dict(T=513, ws=262144, ws_bytes=64), 1), (dict(T=513, ws_bytes=1 << 30), 1),
-    (dict(T=513, ws=262148, ws_bytes=1 << 30), 1), (dict(ws_bytes=-1), 1), (dict(base=65538), 1), (dict(scale=33282), 1), (dict(T=0, x=None), 0),
+    (dict(T=1025), 1), (dict(T=1025, ws=262144, ws_bytes=64), 1), (dict(T=1025, ws_bytes=1 << 30), 1),
+    (dict(T=1025, ws=262148, ws_bytes=1 << 30), 1), (dict(ws_bytes=-1), 1), (dict(base=65538), 1), (dict(scale=33282), 1), (dict(T=0, x=None), 0),
 ])
 def test_refusals(pw, change, status):
     L = pw.lib()
@@ -283,9 +283,9 @@ def test_refusals(pw, change, status):
 
 def test_workspace_bytes(pw):
     size = pw.lib().pw_adapters_workspace_bytes
-    assert size(1, 16, 0) == 0 and size(512, 256, 0) == 0 and size(513, 0, 0) == 0
-    assert size(513, 16, 0) > size(513, 16, 1) > 0
-    assert size(4096, 64, 0) == 64 * (size(576, 64, 0) // 9)
+    assert size(1, 16, 0) == 0 and size(1024, 256, 0) == 0 and size(1025, 0, 0) == 0
+    assert size(1025, 16, 0) > size(1025, 16, 1) > 0
+    assert size(4096, 64, 0) == 64 * (size(1088, 64, 0) // 17)
 
 
 def test_binding_refuses_cpu_tensors(pw):
