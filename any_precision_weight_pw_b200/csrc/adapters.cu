@@ -1,26 +1,33 @@
 // adapters.cu -- pw_adapters: low-rank adapters of many requests beside one
 // shared projection, y_t = base_t + scale_a * B_a (A_a x_t), a = ids[t].
 //
-// Both products run on mma.sync m16n8k16 (bf16, fp32 accumulation) straight
-// from global memory: the contraction index may be permuted freely as long as
-// both operands agree, so each lane loads 16 (shrink, v = A x) or 8 (expand,
-// y += B v) contiguous bytes of a row and uses them as its fragments of two or
-// one MMA steps.  At ranks up to 64 the operator needs at most about 50
-// operations a byte, a fifth of what this GPU's tensor cores could do per byte
-// of its memory, so the wide tcgen05 tiles, which would need x, B and base
-// staged in shared memory, have nothing to win here; what counts is bytes in
-// flight and the length of the chain of dependent loads.
+// The tokens of a window of 256 are taken in the order of their adapters (those
+// without one last), so tokens that share an adapter share its reads.
 //
-// The tokens of a window of 256 are taken in the order of their adapters, and
-// cut into pieces of at most 16 tokens of one adapter (the rows of an MMA
-// tile): tokens that share an adapter share its reads.
-//   Few tokens (at most kNarrow): one launch, a cluster of 8 blocks per piece,
-//     each an eighth of the columns, then of the rows; v's partial sums meet
-//     over distributed shared memory.  What the second product reads besides v
-//     is loaded before the barrier.
-//   Many tokens: shrink_kernel, clusters of 8 over 64 ordered tokens, leaves v
-//     and the pieces in the workspace; expand_kernel walks (64 tokens) x (512
-//     rows) tiles, all equal work, next base tile in flight.
+// Up to kNarrow tokens: one launch, a cluster of 8 blocks for each piece of at
+// most 16 tokens of one adapter.  Each block takes an eighth of the columns of
+// v = A x, the partial sums meet over distributed shared memory, then it takes
+// an eighth of the rows of y = base + B v; B and base are in flight over the
+// exchange.  Both products run on mma.sync straight from global memory: the
+// contraction index may be permuted freely as long as both operands agree, so a
+// lane loads 16 contiguous bytes of a row and uses them as its fragments of two
+// MMA steps.  At this size the chain of dependent loads bounds the kernel, not
+// the products.  (Staging through shared memory for wide tcgen05 tiles would
+// lengthen the chain.)
+//
+// Above: two launches.  shrink_kernel leaves v of each 64 ordered tokens in the
+// workspace, expand_kernel adds B v to (64 tokens) x (some 128 rows) tiles.
+// Both products run on tcgen05: mma.sync did the second at a sixth of the
+// tensor cores' rate and took 50 of 141 us at 4096 tokens x 14336 rows, rank 64
+// (110 with tcgen05; base and y alone, 470 MB, take 93).  Measured there as a
+// whole, 4096 columns, 8 requests: 133 us, 59% of the floor of 78.  The other
+// bound is base and y: 512-byte runs of 64 rows, with two blocks an SM.
+//
+// 512 tokens are the border where both take the same time with one request a
+// tile; with requests that end inside tiles the one launch wins up to 1024 (517
+// tokens of 9 requests, 1409 -> 1003: 16 us against 32; 1024 of 8, 4096 ->
+// 4096, rank 16: 29 against 37, rank 64: 44 against 39).
+//
 // Every sum has a fixed order: results do not depend on timing.
 //
 // Precision.  v is split into bf16 terms (v = hi + mid + lo, 24 bits; two
@@ -1298,8 +1305,8 @@ extern "C" pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const 
   using namespace pw;
   auto bad = [](const char* msg) { return record_error(PW_ERR_INVALID_ARG, msg); };
   if (T < 0 || cols < 1 || rows < 1) return bad("pw_adapters: need T >= 0, cols >= 1, rows >= 1");
-  if (cols > (1 << 30) || rows > (1 << 30))
-    return record_error(PW_ERR_UNSUPPORTED, "pw_adapters: cols or rows above 2^30");
+  if (cols > (1 << 28) || rows > (1 << 28))
+    return record_error(PW_ERR_UNSUPPORTED, "pw_adapters: cols or rows above 2^28");
   if (n_adapters < 1 || n_adapters > PW_MAX_ADAPTERS)
     return bad("pw_adapters: need 1 <= n_adapters <= 4194303");
   if (max_rank < 1 || max_rank > PW_MAX_ADAPTER_RANK)

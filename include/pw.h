@@ -452,7 +452,9 @@ pw_status_t pw_token_logprobs(const void* d_logits, int32_t logits_type, int64_t
  * 1 <= max_rank <= PW_MAX_ADAPTER_RANK.  d_workspace: device memory of
  * workspace_bytes >= pw_adapters_workspace_bytes (0 up to 1024 tokens, then
  * NULL is accepted), 16-byte aligned, used by this call alone until its work
- * is done; its contents need not be set or kept. */
+ * is done; its contents need not be set or kept.  cols and rows up to 2^28
+ * (PW_ERR_UNSUPPORTED above).  Device waits are bounded as pw_linear's: one
+ * that gives up leaves d_y unspecified without a report. */
 #define PW_MAX_ADAPTER_RANK 256
 #define PW_MAX_ADAPTERS 4194303
 pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const uint16_t* d_a,
