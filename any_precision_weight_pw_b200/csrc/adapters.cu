@@ -20,7 +20,7 @@
 // Both products run on tcgen05: mma.sync did the second at a sixth of the
 // tensor cores' rate and took 50 of 141 us at 4096 tokens x 14336 rows, rank 64
 // (110 with tcgen05; base and y alone, 470 MB, take 93).  Measured there as a
-// whole, 4096 columns, 8 requests: 133 us, 59% of the floor of 78.  The other
+// whole, 4096 columns, 8 requests: 117 us, 67% of the floor of 78.  The other
 // bound is base and y: 512-byte runs of 64 rows, with two blocks an SM.
 //
 // 512 tokens are the border where both take the same time with one request a
@@ -579,9 +579,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -664,20 +661,22 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-constexpr int kShrinkStages = 5;
-constexpr int kShrinkStage = 2 * 64 * 128;  // bytes: x [64][64], A [64][64]
+constexpr int kShrinkStages = 3;
+constexpr int kShrinkStage = 3 * 64 * 128;  // bytes: x [64][64], A [64][64] of two segments
 constexpr int kChains = 4;                  // accumulators the steps of a pass go to in turn
 constexpr int kTmemCols = 64 * kChains;
 
 // v of 64 ordered tokens: a cluster of p.split blocks, each its share of the
-// columns.  Per segment and 64 ranks: D[token][rank] = x [64][64] A^T over the block's
-// 64-column steps on tcgen05, copied four steps ahead.  The MMA has 128 rows;
-// the upper 64 run over the A tile behind x and are not used (the tensor cores
-// have the time: half a percent of it is used).  Partial sums go to the block
-// that owns the tokens, which adds them in rank order.  The tensor cores cut
-// their sums off instead of rounding them: the steps go to four accumulators in
-// turn, which keeps the chains short (one: 1.1e-6 relative error of y at 4096
-// columns and rank 64).
+// columns.  A pass takes two neighbouring segments and 64 ranks: D[token][rank]
+// = x [64][64] A_s^T over the block's 64-column steps on tcgen05, x once for
+// both, copied two steps ahead; a token takes its own segment's D (tiles on the
+// border of two requests in one pass: the operator 133 -> 117 us at 4096 tokens
+// of 8 requests, 4096 -> 14336, rank 64).  The MMA has 128 rows; the upper 64 run over the A tile behind x
+// and are not used (the tensor cores have the time).  Partial sums go to the
+// block that owns the tokens, which adds them in rank order.  The tensor cores
+// cut their sums off instead of rounding them: the steps go to two (two
+// segments) or four accumulators in turn, which keeps the chains short (one:
+// 1.1e-6 relative error of y at 4096 columns and rank 64).
 template <bool VEC>
 __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterParams p) {
   constexpr int STAGES = kShrinkStages;
@@ -751,53 +750,72 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
   const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * kb_all / split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * kb_all / split);
   const int n_segments = s_info.n_segments, n_steps = kb1 - kb0;
-  // The copies run ahead over the passes (a segment's 64 ranks each), with
-  // their own place: rows `row` and row + 32 of both tiles, one 16-byte piece
-  // of each step.
+  // A pass: segments g0 and g0 + 1 of the tile, ranks [r0, r0 + 64).
+  struct Pass {
+    int start, len, len0;  // tokens of both, of the first
+    int rank[2], adapter[2];
+  };
+  auto pass_of = [&](int g0) {
+    const Piece s0 = s_info.segment[g0];
+    Pass w = {s0.start, s0.len, s0.len, {s0.rank, 0}, {s0.adapter, -1}};
+    if (g0 + 1 < n_segments) {
+      const Piece s1 = s_info.segment[g0 + 1];
+      w.len += s1.len;
+      w.rank[1] = s1.rank;
+      w.adapter[1] = s1.adapter;
+    }
+    return w;
+  };
+  // The copies run ahead over the passes, with their own place: rows `row` and
+  // row + 32 of the three tiles, one 16-byte piece of each step.
   const int row = tid >> 3, pc = tid & 7;
-  const uint32_t off = operand_off(row, pc);  // row + 32: 4096 behind; A: 8192
-  int l_seg = 0, l_r0 = 0, l_i = 0, l_stage = 0, l_col = 0;
-  const uint16_t* l_src[4] = {};  // x[row], x[row + 32], A[row], A[row + 32] at this step
-  bool l_on[4] = {};
+  const uint32_t off = operand_off(row, pc);  // row + 32: 4096 behind; the next tile: 8192
+  int l_g0 = 0, l_r0 = 0, l_i = 0, l_stage = 0, l_col = 0, l_rank = 0;
+  const uint16_t* l_src[6] = {};  // x, A of the first, of the second; row and row + 32
+  bool l_on[6] = {};
   auto issue = [&]() {
-    if (l_i == 0) {
-      while (l_seg < n_segments && s_info.segment[l_seg].rank == 0) ++l_seg;
-      if (l_seg < n_segments) {
-        const Piece sg = s_info.segment[l_seg];
+    while (l_i == 0 && l_r0 == 0 && l_g0 < n_segments) {  // the next pair with a rank
+      const Pass w = pass_of(l_g0);
+      l_rank = max(w.rank[0], w.rank[1]);
+      if (l_rank > 0) break;
+      l_g0 += 2;
+    }
+    if (l_g0 < n_segments) {
+      if (l_i == 0) {
+        const Pass w = pass_of(l_g0);
         l_col = kb0 * 64 + pc * 8;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = row + 32 * h;
-          l_on[h] = r < sg.len;
-          l_src[h] = p.x + tok[sg.start + min(r, sg.len - 1)] * p.x_ld;
-          l_on[2 + h] = l_r0 + r < sg.rank;
-          l_src[2 + h] = p.a + (static_cast<int64_t>(sg.adapter) * p.r_max + l_r0 + r) * p.cols;
+          l_on[h] = r < w.len;
+          l_src[h] = p.x + tok[w.start + min(r, w.len - 1)] * p.x_ld;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            l_on[2 + 2 * j + h] = l_r0 + r < w.rank[j];
+            l_src[2 + 2 * j + h] =
+                p.a + (static_cast<int64_t>(max(w.adapter[j], 0)) * p.r_max + l_r0 + r) * p.cols;
+          }
         }
       }
-    }
-    if (l_seg < n_segments) {
       const uint32_t at = l_stage * kShrinkStage + off;
-      if (VEC && (kb0 + l_i + 1) * 64 <= p.cols) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-          if (l_on[h]) cp_async16(sm + at + h * 4096, l_src[h] + l_col);
-      } else {
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-          if (l_on[h]) {
-            if constexpr (VEC)
-              cp_async16(sm + at + h * 4096, l_col < p.cols ? l_src[h] + l_col : p.x,
-                         l_col < p.cols ? 16 : 0);
-            else
-              *reinterpret_cast<uint4*>(smp + at + h * 4096) = load8<false>(l_src[h], l_col, p.cols);
-          }
-      }
+      for (int h = 0; h < 6; ++h)
+        if (l_on[h]) {
+          if constexpr (VEC)
+            cp_async16(sm + at + h * 4096, l_col < p.cols ? l_src[h] + l_col : p.x,
+                       l_col < p.cols ? 16 : 0);
+          else
+            *reinterpret_cast<uint4*>(smp + at + h * 4096) = load8<false>(l_src[h], l_col, p.cols);
+        }
       l_col += 64;
       l_stage = l_stage + 1 == STAGES ? 0 : l_stage + 1;
       if (++l_i == n_steps) {
         l_i = 0;
         l_r0 += 64;
-        if (l_r0 >= s_info.segment[l_seg].rank) l_r0 = 0, ++l_seg;
+        if (l_r0 >= l_rank) {
+          l_r0 = 0;
+          l_g0 += 2;
+        }
       }
     }
     __syncwarp();
@@ -813,12 +831,17 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
   auto wait_step = [&](uint32_t n) { mbar_wait(bar + (n & 1) * 8, n >> 1 & 1, &s_gave_up); };
   int stage = 0;
   bool sums_read = false;  // an arrive without its wait: this block has read its sums
-  for (int seg = 0; seg < n_segments; ++seg) {
-    const Piece sg = s_info.segment[seg];
-    const float sc = sg.adapter >= 0 && p.scale ? p.scale[sg.adapter] : 1.f;
-    for (int r0 = 0; r0 < sg.rank; r0 += 64) {
-      const int n_r = min(64, sg.rank - r0);
-      const uint32_t idesc = mma_idesc((n_r + 15) / 16 * 16);
+  for (int g0 = 0; g0 < n_segments; g0 += 2) {
+    const Pass w = pass_of(g0);
+    float sc[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      sc[j] = w.adapter[j] >= 0 && p.scale ? p.scale[w.adapter[j]] : 1.f;
+    for (int r0 = 0; r0 < max(w.rank[0], w.rank[1]); r0 += 64) {
+      const int n_r[2] = {min(64, w.rank[0] - r0), min(64, w.rank[1] - r0)};  // none if <= 0
+      // accumulators: chain c of segment j at 64 (per * j + c)
+      const int per = n_r[0] > 0 && n_r[1] > 0 ? kChains / 2 : kChains;
+      const int second = per == kChains ? 0 : 64 * per;
       for (int i = 0; i < n_steps; ++i) {
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -827,10 +850,17 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
           tc_fence_after();
           if (elect_one()) {
             const uint32_t at = sm + stage * kShrinkStage;
-            const uint64_t dx = operand_desc(at), da = operand_desc(at + 8192);
+            const uint64_t dx = operand_desc(at);
+            const uint32_t d = tmem + i % per * 64;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma(tmem + i % kChains * 64, dx + 2 * k, da + 2 * k, idesc, i >= kChains || k > 0);
+            for (int j = 0; j < 2; ++j) {
+              if (n_r[j] <= 0) continue;
+              const uint64_t da = operand_desc(at + 8192 * (1 + j));
+              const uint32_t idesc = mma_idesc((n_r[j] + 15) / 16 * 16);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma(d + j * second, dx + 2 * k, da + 2 * k, idesc, i >= per || k > 0);
+            }
             asm volatile(
                 "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                     bar + (n_done & 1) * 8)
@@ -845,26 +875,31 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
       }
       if (n_steps > 0) wait_step(n_done - 1);
       if (sums_read) cluster_wait();  // the last sums have been read everywhere
-      // token 32 warp + lane of the accumulator to its owner
-      if (warp < 2 && warp * 32 < sg.len) {
+      // token 32 warp + lane of its segment's accumulators to its owner
+      if (warp < 2 && warp * 32 < w.len) {
         const int t = warp * 32 + lane;
         const uint32_t d = in_block(smem_u32(slots + (rank * own + t % own) * 64), t / own);
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (32 * h >= n_r) break;
           float v[32] = {};
-          for (int i = 0; i < min(n_steps, kChains); ++i) {
-            float w[32];
-            tmem_ld32(tmem + (static_cast<uint32_t>(warp) * 32 << 16) + i * 64 + 32 * h, w);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += w[j];
+          for (int j = 0; j < 2; ++j) {
+            // the same for the warp: the segment has ranks here and tokens among these 32
+            if (32 * h >= n_r[j] || (j == 0 ? warp * 32 >= w.len0 : warp * 32 + 32 <= w.len0)) continue;
+            const bool mine = (t >= w.len0) == (j == 1);
+            for (int c = 0; c < min(n_steps, per); ++c) {
+              float u[32];
+              tmem_ld32(tmem + (static_cast<uint32_t>(warp) * 32 << 16) + j * second + c * 64 + 32 * h, u);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = mine ? v[e] + u[e] : v[e];
+            }
           }
-          if (t < sg.len)
+          if (t < w.len)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              put4(d + (32 * h + 4 * j) * 4,
-                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+            for (int e = 0; e < 8; ++e)
+              put4(d + (32 * h + 4 * e) * 4,
+                   make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
         }
         tc_fence_before();
       }
@@ -873,16 +908,19 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
       // sums over the blocks; scale v and split it into bf16 terms
       for (int e = tid * 2; e < own * 64; e += kAdThreads * 2) {
         const int t = rank * own + e / 64, k = e % 64;
-        if (t >= sg.len || r0 + k >= p.r32) continue;
+        const bool two = t >= w.len0;
+        const int n = two ? n_r[1] : n_r[0];
+        if (t >= w.len || n <= 0 || r0 + k >= p.r32) continue;
         float v[2] = {0.f, 0.f};
         for (int c = 0; c < split; ++c) {
-          const float2 w = *reinterpret_cast<const float2*>(slots + c * own * 64 + e);
-          v[0] += w.x, v[1] += w.y;
+          const float2 u = *reinterpret_cast<const float2*>(slots + c * own * 64 + e);
+          v[0] += u.x, v[1] += u.y;
         }
-        v[0] = k < n_r ? v[0] * sc : 0.f;
-        v[1] = k + 1 < n_r ? v[1] * sc : 0.f;
+        const float f = two ? sc[1] : sc[0];
+        v[0] = k < n ? v[0] * f : 0.f;
+        v[1] = k + 1 < n ? v[1] * f : 0.f;
         for (int i = 0; i < p.n_terms; ++i)
-          *reinterpret_cast<uint32_t*>(vt + i * v_plane + (sg.start + t) * p.v_ld + r0 + k) =
+          *reinterpret_cast<uint32_t*>(vt + i * v_plane + (w.start + t) * p.v_ld + r0 + k) =
               next_term(v);
       }
       // relaxed: nothing is handed over (a release would wait for v's stores)
