@@ -278,20 +278,34 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
     stats();
     group_max();
     row_reduce(ss, mx, tpr, part[parity]);
-    if (isinf(ss)) {
-      // the squares left fp32's range: once more on h * 2^-80, whose squares
-      // cannot (|h| < 2^128, 2^15 columns); y does not depend on the factor
-      // but through eps, far below such a mean
+    float rstd = 1.0f / sqrtf(fmaf(ss, p.inv_h, p.eps));
+    if (isinf(ss)) {  // the same for the row
+      // The squares left fp32's range: once more on h * f, f = 2^-80, whose
+      // squares cannot (|h| < 2^128, 2^15 columns).  With the mean scaled by f^2,
+      // eps is too: a row that only just overflows has a scaled mean near
+      // 2^-47, far below a usual eps as it stands.  The row then becomes
+      // h / rms, where 1 / rms alone could be subnormal.
+      constexpr float f = 8.271806125530277e-25f;
+      ss = 0.f;
 #pragma unroll
       for (int j = 0; j < M; ++j)
 #pragma unroll
-        for (int k = 0; k < N; ++k) h[j][k] *= 8.271806125530277e-25f;  // 2^-80
+        for (int k = 0; k < N; ++k) ss = fmaf(h[j][k] * f, h[j][k] * f, ss);
       parity ^= 1;
-      stats();
-      group_max();
       row_reduce(ss, mx, tpr, part[parity]);
+      rstd = 1.0f / sqrtf(fmaf(ss, p.inv_h, p.eps * f * f));
+#pragma unroll
+      for (int j = 0; j < M; ++j)
+#pragma unroll
+        for (int k = 0; k < N; ++k) h[j][k] = h[j][k] * rstd * f;
+      rstd = 1.0f;
+      if constexpr (OUT != kOutBf16) {
+        parity ^= 1;
+        stats();
+        group_max();
+        row_reduce(ss, mx, tpr, part[parity]);
+      }
     }
-    const float rstd = 1.0f / sqrtf(fmaf(ss, p.inv_h, p.eps));
     if (!live) continue;
     if constexpr (OUT == kOutE4m3Row) {
       const float s = max_nan(mx * rstd / kE4m3Max, kScaleMin);

@@ -160,6 +160,33 @@ def test_zero_huge_and_nonfinite_rows(gpu, H, out, group):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H", [64, 1409, 4096, 9001, 32768])
+@pytest.mark.parametrize("xt,rt", [(BF16, BF16), (F32, None)])
+@pytest.mark.parametrize("out,group", [(BF16, 0), (E4M3, 0), (E4M3, 128)])
+@pytest.mark.parametrize("eps", [EPS, 2.0 ** 120])
+def test_rows_around_the_overflow_of_squares(gpu, H, xt, rt, out, group, eps):
+    """Rows from 2^48 to 2^124, so that sums of squares pass fp32's largest
+    value on the way, each with a first element far below the others; eps from
+    negligible to the larger term of the mean.  2^-133 is a step of the smallest
+    bf16 values."""
+    gen = torch.Generator().manual_seed(H)
+    size = 2.0 ** torch.arange(48, 126, 2).double()
+    T = len(size)
+    x = torch.randn((T, H), generator=gen).clamp(-4, 4).double() * size[:, None]
+    x[:, 0] = 2.0 ** -30
+    x = x.to(xt).cuda()
+    res = None if rt is None else (rows(gen, T, H, rt) * 0.25).to(rt)
+    w = (torch.randn(H, generator=gen) * 0.2 + 1).to(BF16).cuda()
+    y, s, _ = gpu.add_rms_norm(x, w, eps, residual=res, y_type=out, scale_group=group)
+    h = x.double() if res is None else x.double() + res.double()
+    want = h / torch.sqrt((h * h).mean(1, keepdim=True) + eps) * w.double()
+    if out == BF16:
+        assert ((y.double() - want).abs() <= want.abs() * (2.0 ** -8 + ARITH) + 2.0 ** -133).all()
+    else:
+        check_e4m3(y, s, want, group)
+
+
+@pytest.mark.gpu
 def test_streams_capture_and_empty(gpu):
     gen = torch.Generator().manual_seed(1)
     x, res = rows(gen, 40, 520, BF16), rows(gen, 40, 520, BF16)
