@@ -230,7 +230,7 @@ _torch = None
 def _bind() -> None:
     """Module names used on every call: torch, its types' pw_dtype_t codes
     (int16 / uint8 stand for bf16 / e4m3 bit patterns), the current stream."""
-    global _torch, _types, _f32, _i32, _bf16, _bf16_like, _like
+    global _torch, _types, _f32, _i32, _bf16, _bf16_like, _like, _dense
     global _current_device, _current_stream
     import torch
     _f32, _i32, _bf16, _bf16_like = (torch.float32, torch.int32, torch.bfloat16,
@@ -238,6 +238,9 @@ def _bind() -> None:
     _types = {_f32: 0, _bf16: 1, torch.int16: 1, torch.float16: 2, torch.float8_e4m3fn: 3,
               torch.uint8: 3}
     _like = torch.empty_like  # the shortest way to a new tensor
+    # empty_like keeps the order of strides (rows that overlap one element
+    # apart give columns one apart); outputs are rows one after the other
+    _dense = torch.contiguous_format
     _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     # the handle alone: torch.cuda.current_stream() makes a Stream object, 3 us
     _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -321,14 +324,14 @@ def add_rms_norm(x, weight, eps: float, residual=None, residual_out=None, y=None
         r_ld = _rows(residual, "residual", shape, dev, (0, 1))
         r_code, res = _types[residual.dtype], residual.data_ptr()
         if residual_out is None:
-            residual_out, ro_ld = _like(residual), H
+            residual_out, ro_ld = _like(residual, memory_format=_dense), H
         else:
             ro_ld = _rows(residual_out, "residual_out", shape, dev, (r_code,))
         r_out = residual_out.data_ptr()
     elif residual_out is not None:
         _refuse("residual_out: needs a residual")
     if y is None:
-        y, y_ld = _like(x, dtype=y_type or _bf16), H
+        y, y_ld = _like(x, dtype=y_type or _bf16, memory_format=_dense), H
     else:
         if y_type is not None and _types.get(y.dtype) != _types.get(y_type):
             _refuse("y: type %s, y_type %s" % (y.dtype, y_type))
@@ -439,7 +442,8 @@ def add_adapters(x, a, b, ids, base=None, scale=None, ranks=None, y=None, y_type
         pbase = base.data_ptr()
     if y is None:
         y_ld = rows
-        y = _like(base) if base is not None else x.new_empty(shape, dtype=y_type or _f32)
+        y = (_like(base, memory_format=_dense) if base is not None else
+             x.new_empty(shape, dtype=y_type or _f32))
     else:
         y_ld = _rows(y, "y", shape, dev, (0, 1) if base is None else (_types[base.dtype],))
     y_code = _types.get(y.dtype)

@@ -136,6 +136,19 @@ def test_base_forms(gpu, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,rows", [(8, 64), (64, 8), (1100, 24)])
+def test_base_rows_that_overlap(gpu, T, rows):
+    """A base whose rows are one element apart: y is row after row."""
+    gen = torch.Generator().manual_seed(T)
+    d = make(gen, T, 64, rows, 3, 8)
+    d["base"] = torch.randn(T + rows - 1, generator=gen).cuda().unfold(0, rows, 1)
+    assert d["base"].stride() == (1, 1)
+    y = gpu.add_adapters(**d)
+    assert y.is_contiguous()
+    assert torch.equal(y, gpu.add_adapters(**{**d, "base": d["base"].contiguous()}))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [6, 2100])
 def test_nonfinite_values_stay_in_their_token(gpu, T):
     """NaN and infinities of a token, of an adapter or of unused ranks reach

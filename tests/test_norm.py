@@ -160,6 +160,21 @@ def test_zero_huge_and_nonfinite_rows(gpu, H, out, group):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [(8, 64), (64, 8), (5, 130), (2, 1409)])
+def test_rows_that_overlap(gpu, T, H):
+    """Windows of a series: rows one element apart, outputs row after row."""
+    gen = torch.Generator().manual_seed(T)
+    series = torch.randn(T + H - 1, generator=gen).cuda()
+    x = series.unfold(0, H, 1)
+    assert x.shape == (T, H) and x.stride() == (1, 1)
+    res, w = (series * 2).unfold(0, H, 1), torch.ones(H, device="cuda")
+    y, _, ro = gpu.add_rms_norm(x, w, EPS, residual=res)
+    y2, _, ro2 = gpu.add_rms_norm(x.contiguous(), w, EPS, residual=res.contiguous())
+    assert torch.equal(y, y2) and torch.equal(ro, ro2)
+    assert y.is_contiguous() and ro.is_contiguous()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("H", [64, 1409, 4096, 9001, 32768])
 @pytest.mark.parametrize("xt,rt", [(BF16, BF16), (F32, None)])
 @pytest.mark.parametrize("out,group", [(BF16, 0), (E4M3, 0), (E4M3, 128)])
