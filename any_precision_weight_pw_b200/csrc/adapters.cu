@@ -543,7 +543,10 @@ __global__ void __launch_bounds__(kAdThreads, 2) adapter_kernel(const AdapterPar
         const float2 o = *reinterpret_cast<const float2*>(slot + c * kTile + e);
         v[0] += o.x, v[1] += o.y;
       }
-      v[0] *= sc, v[1] *= sc;
+      // from the adapter's rank on v is zero, also where x or the scale is not
+      // finite (inf times the zeros read for A there is NaN)
+      v[0] = k < pc.rank ? v[0] * sc : 0.f;
+      v[1] = k + 1 < pc.rank ? v[1] * sc : 0.f;
 #pragma unroll
       for (int t = 0; t < Tile::kTerms; ++t) {
         uint16_t* d = vt + t * v_plane + row * p.v_ld + k;

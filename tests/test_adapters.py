@@ -181,6 +181,34 @@ def test_nonfinite_values_stay_in_their_token(gpu, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 6, 600, 2100])
+@pytest.mark.parametrize("r,rank", [(16, 1), (16, 16), (20, 3), (64, 1), (72, 70), (256, 9)])
+@pytest.mark.parametrize("y", [F32, BF16])
+def test_infinite_x_or_scale_stays_infinite(gpu, T, r, rank, y):
+    """No unused rank turns an infinity of x or of a scale into NaN: A and B
+    are positive, so outputs are infinite with the sign of v."""
+    gen = torch.Generator().manual_seed(T + r)
+    d = make(gen, T, 136, 72, 2, r, y)
+    d["a"], d["b"] = d["a"].abs() + 0.01, d["b"].abs() + 0.01
+    d["a"][1, rank:] = -1.0
+    d["b"][1, :, rank:] = float("nan")
+    d["ranks"] = torch.tensor([r, rank], dtype=torch.int32, device="cuda")
+    d["ids"] = (torch.arange(T, device="cuda") % 2 == 0).int()
+    d["x"] = d["x"].abs()
+    d["x"][0, 5] = float("inf")
+    d["x"][T - 1 - (T - 1) % 2, 135] = float("-inf") if T > 2 else float("inf")
+    got = gpu.add_adapters(**d)
+    assert (got[0] == float("inf")).all()
+    if T > 2:
+        assert (got[T - 1 - (T - 1) % 2] == float("-inf")).all()
+        assert got[2 if T > 600 else 1].isfinite().all()
+    d["x"] = d["x"].clamp(-4, 4)
+    d["scale"][1] = float("inf")
+    got = gpu.add_adapters(**d)
+    assert (got[::2] == float("inf")).all() and got[1::2].isfinite().all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [20, 2100])
 @pytest.mark.parametrize("y,pad", [(F32, 3), (F32, 8), (BF16, 5), (BF16, 4)])
 def test_strides_alignment_and_gaps(gpu, T, y, pad):
