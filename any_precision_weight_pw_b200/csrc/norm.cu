@@ -166,8 +166,11 @@ __device__ __forceinline__ void row_reduce(float& a, float& b, int tpr, float2* 
 
 // One row per tpr threads, M vectors of N columns a thread.  Vector v of a row
 // belongs to thread v % tpr: a warp's accesses are contiguous.
+// One block an SM is named as the least: without it the compiler takes 32
+// registers for some forms that spill anyway (above 8192 columns), in the hope
+// of two (2048 x 20480 bf16: 184 us against 100; 2048 x 14335: 610 against 522).
 template <typename XT, typename RT, int OUT, int N, int M>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const NormParams p) {
   extern __shared__ float gmax[];  // N = 1 group scales: [2][M * tpr / 32] warp maxima
   __shared__ float2 part[2][32];
   const int tpr = p.tpr, lane_r = threadIdx.x % tpr, rows_blk = blockDim.x / tpr;
