@@ -258,10 +258,11 @@ __device__ __forceinline__ uint32_t next_term(float (&v)[2]) {
   return h[0] | static_cast<uint32_t>(h[1]) << 16;
 }
 
-// 16 tokens x 16 rows of the second product.  MMA column g of tile j is row
-// o + 4 (g / 2) + 2 j + g % 2: a lane then holds rows 4q..4q+3, whole 16-byte
-// accesses of base and y.  A lane holds ranks 8q..8q+7 of each 32 (two MMA
-// steps), whole 16-byte accesses of B and v.
+// 16 tokens x 16 rows of the second product, y = base - B (-v): v is kept
+// negated, so that a sum of nothing, +0, leaves base as it is, -0 too.  MMA
+// column g of tile j is row o + 4 (g / 2) + 2 j + g % 2: a lane then holds rows
+// 4q..4q+3, whole 16-byte accesses of base and y.  A lane holds ranks 8q..8q+7
+// of each 32 (two MMA steps), whole 16-byte accesses of B and v.
 // KS: 32-rank steps.  F32: type of base and y.  VEC: every access is aligned.
 template <int KS, bool F32, bool VEC>
 struct ExpandTile {
@@ -367,7 +368,7 @@ struct ExpandTile {
         v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xffff0000u);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += acc[i >> 1][2 * h + (i & 1)];
+      for (int i = 0; i < 4; ++i) v[i] -= acc[i >> 1][2 * h + (i & 1)];
       E* dst = l.y[h] + ob * 16;
       if constexpr (VEC) {
         if constexpr (F32)
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(kAdThreads, 2) adapter_kernel(const AdapterPar
   const int kb0 = rank * kb_all / kAdCluster, kb1 = (rank + 1) * kb_all / kAdCluster;
   const int ob0 = rank * ob_all / kAdCluster + warp, ob1 = (rank + 1) * ob_all / kAdCluster;
   const int v_plane = 16 * p.v_ld;
-  const float sc = pc.adapter >= 0 && p.scale ? p.scale[pc.adapter] : 1.f;
+  const float minus = pc.adapter >= 0 && p.scale ? -p.scale[pc.adapter] : -1.f;
 
   using Tile = ExpandTile<KS, F32, VEC>;
   const typename Tile::Lane l(p, pc, tok, vt);
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(kAdThreads, 2) adapter_kernel(const AdapterPar
     }
     cluster_arrive();
     cluster_wait();
-    // sums over the blocks; scale v and split it into bf16 terms
+    // sums over the blocks; scale v, negate it and split it into bf16 terms
     for (int e = tid * 2; e < pc.len * kChunk; e += kAdThreads * 2) {
       const int row = e / kChunk, k = r0 + e % kChunk;
       if (k >= p.r32) continue;
@@ -545,8 +546,8 @@ __global__ void __launch_bounds__(kAdThreads, 2) adapter_kernel(const AdapterPar
       }
       // from the adapter's rank on v is zero, also where x or the scale is not
       // finite (inf times the zeros read for A there is NaN)
-      v[0] = k < pc.rank ? v[0] * sc : 0.f;
-      v[1] = k + 1 < pc.rank ? v[1] * sc : 0.f;
+      v[0] = k < pc.rank ? v[0] * minus : 0.f;
+      v[1] = k + 1 < pc.rank ? v[1] * minus : 0.f;
 #pragma unroll
       for (int t = 0; t < Tile::kTerms; ++t) {
         uint16_t* d = vt + t * v_plane + row * p.v_ld + k;

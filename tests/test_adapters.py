@@ -209,6 +209,30 @@ def test_infinite_x_or_scale_stays_infinite(gpu, T, r, rank, y):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 5, 600, 2100])
+@pytest.mark.parametrize("y", [F32, BF16])
+@pytest.mark.parametrize("rows", [72, 37])
+def test_base_keeps_its_bits(gpu, T, y, rows):
+    """Tokens without an adapter, or of one with rank 0, keep base bit for
+    bit, signed zeros and subnormals too (a NaN stays some NaN); also in place."""
+    gen = torch.Generator().manual_seed(T + rows)
+    d = make(gen, T, 64, rows, 3, 16, y, ranks=False)
+    d["ranks"] = torch.tensor([0, 16, 16], dtype=torch.int32, device="cuda")
+    d["ids"] = (torch.arange(T, device="cuda") // 3 % 3 - 1).int()       # none, rank 0, rank 16
+    word = torch.int32 if y == F32 else torch.int16
+    raw = d["base"].view(word)
+    raw[:, 4:7] = torch.tensor([torch.iinfo(word).min, 1, torch.iinfo(word).min + 1], dtype=word)  # -0, +-least
+    d["base"][:, 3] = float("nan")
+    kept = (d["ids"] <= 0).nonzero()[:, 0]
+    want = raw[kept][:, 4:].clone()
+    got = gpu.add_adapters(**d)
+    assert torch.equal(got.view(word)[kept][:, 4:], want)
+    assert got[:, 3].isnan().all() and got[:, 4:].isfinite().all()
+    gpu.add_adapters(**d, y=d["base"])
+    assert torch.equal(raw[kept][:, 4:], want) and d["base"][:, 3].isnan().all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [20, 2100])
 @pytest.mark.parametrize("y,pad", [(F32, 3), (F32, 8), (BF16, 5), (BF16, 4)])
 def test_strides_alignment_and_gaps(gpu, T, y, pad):
