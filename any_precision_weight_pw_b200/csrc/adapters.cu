@@ -570,11 +570,14 @@ __global__ void __launch_bounds__(kAdThreads, 2) adapter_kernel(const AdapterPar
 // What shrink leaves for expand, per 64 tokens: the segments (neighbours of
 // one adapter), the tokens, and v (n_terms planes of [64][v_ld] bf16, by
 // position, zero from the rank on to the next multiple of 32).
-struct TileInfo {
+struct alignas(16) TileInfo {  // moved in 16-byte pieces, in shared memory too
   int n_segments, pad[3];
   Piece segment[kTileTokens];
   int tok[kTileTokens];
 };
+static_assert(alignof(TileInfo) == alignof(uint4) && sizeof(TileInfo) % sizeof(uint4) == 0,
+              "TileInfo is copied as uint4");
+static_assert(sizeof(TileInfo) / sizeof(uint4) <= kAdThreads, "one piece a thread");
 __host__ __device__ __forceinline__ int64_t tile_bytes(int n_terms, int v_ld) {
   return static_cast<int64_t>(sizeof(TileInfo)) + 2ll * n_terms * kTileTokens * v_ld;
 }

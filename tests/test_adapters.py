@@ -353,6 +353,15 @@ def test_workspace_bytes(pw):
     assert size(4096, 64, 0) == 64 * (size(1088, 64, 0) // 17)
 
 
+def test_workspace_tiles_are_whole_16_byte_pieces(pw):
+    """The workspace is read in 16-byte pieces: every tile of it starts on one."""
+    size = pw.lib().pw_adapters_workspace_bytes
+    for r in range(1, 257):
+        for y in (0, 1):
+            tile = size(2048, r, y) - size(1984, r, y)
+            assert tile > 0 and tile % 16 == 0 and size(2048, r, y) == 32 * tile
+
+
 def test_binding_refuses_cpu_tensors(pw):
     with pytest.raises(pw.PwError):
         pw.add_adapters(torch.zeros((2, 8), dtype=BF16), torch.zeros((1, 4, 8), dtype=BF16),
