@@ -487,6 +487,7 @@ class MoELayer:
         check(lib().pw_moe_create(C.byref(c), descs, n, C.byref(h)))
         self.h = h
         self.n_blocks = n
+        self._device = planes[0].get_device()
 
     def forward(self, x, router_w, bias=None, y=None, stream=None):
         import torch
@@ -500,16 +501,37 @@ class MoELayer:
     def forward_norm(self, x, norm_weight, eps: float, router_w, bias=None, residual=None,
                      residual_out=None, y=None, stream=None):
         """forward of x' = add_rms_norm(x, norm_weight, eps, residual): all
-        bf16 and contiguous.  Returns (y, residual_out or None)."""
-        import torch
-        T = x.shape[0]
+        bf16 (int16 bit patterns are taken too) and contiguous, on the layer's
+        device; router_w fp32 [E][H], bias fp32 [E].  residual_out may be the
+        residual.  Every tensor is checked as in the calls above; nothing is
+        enqueued for a refused one.  Returns (y, residual_out or None)."""
+        if _torch is None:
+            _bind()
+        H, E, dev = self.cfg["hidden"], self.cfg["n_experts"], self._device
+        if x.dim() != 2:
+            _refuse("x: [T][H] is needed")
+        rows = (x.shape[0], H)
+        for t, name, shape, types in (
+                (x, "x", rows, _bf16_like), (residual, "residual", rows, _bf16_like),
+                (norm_weight, "norm_weight", (H,), _bf16_like),
+                (residual_out, "residual_out", rows, _bf16_like),
+                (router_w, "router_w", (E, H), (_f32,)), (bias, "bias", (E,), (_f32,)),
+                (y, "y", rows, _bf16_like)):
+            _flat(t, name, shape, dev, types)
+        if norm_weight is None or router_w is None:
+            _refuse("norm_weight and router_w are needed")
+        if residual is None and residual_out is not None:
+            _refuse("residual_out: needs a residual")
+        if stream is not None or dev != _current_device():
+            return _elsewhere(self.forward_norm, dev, stream, x, norm_weight, eps, router_w, bias,
+                              residual, residual_out, y)
         if y is None:
-            y = torch.empty_like(x)
+            y = _like(x)
         if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(residual)
-        check(lib().pw_moe_forward_norm(self.h, _ptr(x), _ptr(residual), _ptr(norm_weight), eps, T,
-                                        _ptr(router_w), _ptr(bias), _ptr(residual_out), _ptr(y),
-                                        _stream(stream)))
+            residual_out = _like(residual)
+        check(lib().pw_moe_forward_norm(self.h, _ptr(x), _ptr(residual), _ptr(norm_weight), eps,
+                                        rows[0], _ptr(router_w), _ptr(bias), _ptr(residual_out),
+                                        _ptr(y), _current_stream(dev)))
         return y, residual_out
 
     def forward_host(self, x_host, router_w, bias=None, y_host=None, stream=None):

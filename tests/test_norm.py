@@ -289,9 +289,78 @@ def test_moe_forward_norm_refuses_null_handle(pw):
                                         None) == 1
 
 
+def layer_without_handle(pw):
+    """A layer of 4 experts x 64 columns without a handle, on the CPU (-1)."""
+    layer = object.__new__(pw.MoELayer)
+    layer.cfg, layer._device, layer.h = dict(hidden=64, n_experts=4), -1, None
+    return layer
+
+
+@pytest.mark.parametrize("change,names", [
+    (dict(residual=torch.zeros(3, 64, dtype=BF16)), "residual: shape"),
+    (dict(x=torch.zeros(5, 63, dtype=BF16)), "x: shape"), (dict(x=torch.zeros(64, dtype=BF16)), "x: "),
+    (dict(norm_weight=torch.zeros(63, dtype=BF16)), "norm_weight: shape"),
+    (dict(router_w=torch.zeros(3, 64)), "router_w: shape"), (dict(bias=torch.zeros(3)), "bias: shape"),
+    (dict(y=torch.zeros(4, 64, dtype=BF16)), "y: shape"),
+    (dict(residual=torch.zeros(5, 64, dtype=BF16), residual_out=torch.zeros(4, 64, dtype=BF16)),
+     "residual_out: shape"),
+    (dict(residual=torch.zeros(5, 64)), "residual: type"), (dict(norm_weight=torch.zeros(64)), "norm_weight: type"),
+    (dict(x=torch.zeros(5, 128, dtype=BF16)[:, ::2]), "x: must be contiguous"),
+    (dict(residual_out=torch.zeros(5, 64, dtype=BF16)), "residual_out: needs a residual"),
+    (dict(norm_weight=None), "are needed"), (dict(router_w=None), "are needed"),
+])
+def test_moe_forward_norm_checks_its_tensors(pw, change, names):
+    """Shapes, types and layouts, by tensors on the CPU; then their device."""
+    a = dict(x=torch.zeros(5, 64, dtype=BF16), norm_weight=torch.zeros(64, dtype=BF16), eps=EPS,
+             router_w=torch.zeros(4, 64))
+    with pytest.raises(pw.PwError) as e:
+        layer_without_handle(pw).forward_norm(**{**a, **change})
+    assert e.value.status == 1 and names in str(e.value)
+    layer = layer_without_handle(pw)
+    layer._device = 0
+    with pytest.raises(pw.PwError, match="x: on another device"):
+        layer.forward_norm(**a)
+
+
 def test_binding_refuses_cpu_tensors(pw):
     with pytest.raises(pw.PwError):
         pw.add_rms_norm(torch.zeros(2, 8), torch.ones(8), EPS)
+
+
+@pytest.mark.gpu
+def test_moe_forward_norm_refusals_and_streams(gpu):
+    """Types, devices and layouts are refused before anything runs; on another
+    stream the outputs are the same."""
+    from any_precision_weight_pw_b200 import synth
+    layer = synth.Layer(synth.WORKLOADS["tiny_h256_f512_e8k2"], seed=0)
+    dev = gpu.upload_synth_layer(layer, max_tokens=16)
+    H = layer.wl.hidden
+    gen = torch.Generator().manual_seed(1)
+    a = dict(x=rows(gen, 5, H, BF16), norm_weight=torch.ones(H, dtype=BF16, device="cuda"), eps=EPS,
+             router_w=torch.from_numpy(layer.router_w).cuda(), residual=rows(gen, 5, H, BF16))
+    want = dev.forward_norm(**a)
+    before = a["residual"].clone()
+    for change in (dict(x=a["x"].float()), dict(x=a["x"].cpu()), dict(residual=a["residual"][:4]),
+                   dict(residual=a["residual"].half()), dict(norm_weight=a["norm_weight"].float()),
+                   dict(norm_weight=a["norm_weight"][:-1]), dict(router_w=a["router_w"].to(BF16)),
+                   dict(router_w=a["router_w"].t().contiguous().t()), dict(bias=a["router_w"][0]),
+                   dict(x=rows(gen, 5, H, BF16, pad=8)), dict(y=torch.empty(5, H, device="cuda")),
+                   dict(residual=None, residual_out=a["x"]), dict(router_w=None), dict(eps=0.0),
+                   dict(x=rows(gen, 17, H, BF16), residual=None)):
+        b = {**a, **change}
+        if b["residual"] is a["residual"]:
+            b["residual_out"] = a["residual"]
+        with pytest.raises(gpu.PwError):
+            dev.forward_norm(**b)
+    torch.cuda.synchronize()
+    assert torch.equal(a["residual"], before)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = dev.forward_norm(**a, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    dev.check_device_error()
+    dev.close()
 
 
 @pytest.mark.gpu
