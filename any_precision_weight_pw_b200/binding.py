@@ -149,16 +149,19 @@ def linear(planes, lut, bits: int, x, rows: int, y=None, stream=None, adapters=N
     lut: int16 [rows][2^bits] (fp16 bit patterns); x: bf16 [T][cols].
     Returns fp32 [T][rows].  With adapters (the keyword arguments of
     add_adapters: a, b and optionally scale, ranks) and adapter_ids, every
-    token's low-rank adapter is added to y in place."""
+    token's low-rank adapter is added to y in place; the adapters, x and y
+    (fp32, contiguous) are then checked before anything is enqueued."""
     import torch
+    if adapters is not None:
+        return _linear_with_adapters(planes, lut, bits, x, rows, y, stream, adapters, adapter_ids)
+    if adapter_ids is not None:
+        raise PwError(1, "adapter_ids: needs adapters")
     T, cols = x.shape
     n_max = planes.numel() * 4 // plane_bytes(rows, cols)
     if y is None:
         y = torch.empty((T, rows), dtype=torch.float32, device=x.device)
     check(lib().pw_linear(_ptr(planes), _ptr(lut), rows, cols, n_max, bits, _ptr(x), T, _ptr(y),
                           _stream(stream)))
-    if adapters is not None:
-        add_adapters(x, ids=adapter_ids, base=y, y=y, stream=stream, **adapters)
     return y
 
 
@@ -292,9 +295,10 @@ def _elsewhere(fn, dev: int, stream, *args):
         _refuse("stream: on another device than the tensors")
     with _torch.cuda.stream(stream):
         out = fn(*args)
-    for t in args:
-        if isinstance(t, _torch.Tensor):
-            t.record_stream(stream)
+    for arg in args:
+        for t in arg.values() if isinstance(arg, dict) else (arg,):
+            if isinstance(t, _torch.Tensor):
+                t.record_stream(stream)
     return out
 
 
@@ -412,7 +416,7 @@ def token_logprobs(logits, tokens=None, n_top: int = 0, logprob=None, entropy=No
 
 
 def add_adapters(x, a, b, ids, base=None, scale=None, ranks=None, y=None, y_type=None,
-                 stream=None):
+                 stream=None, _first=None):
     """y[t] = base[t] + scale[i] * B_i (A_i x[t]), i = ids[t]; base[t] alone
     where ids[t] is -1.
 
@@ -454,12 +458,42 @@ def add_adapters(x, a, b, ids, base=None, scale=None, ranks=None, y=None, y_type
     if size:
         keep = x.new_empty((size,), dtype=_torch.uint8)
         work = keep.data_ptr()
+    stream = _current_stream(dev)
+    if _first is not None:
+        # sizes out of range are refused for no tokens as for some
+        check(L.pw_adapters(None, 0, None, None, None, None, None, n, r, 0, cols, rows, None, 0, None,
+                            y_code, 0, None, 0, None))
+        _first(stream)
     status = L.pw_adapters(x.data_ptr(), x_ld, pa, pb, pi, pr, ps, n, r, T, cols, rows, pbase,
                            base_ld, y.data_ptr(), -1 if y_code is None else y_code, y_ld, work, size,
-                           _current_stream(dev))
+                           stream)
     if status:
         check(status)
     return y
+
+
+def _linear_with_adapters(planes, lut, bits, x, rows, y, stream, adapters, ids):
+    """linear's two calls; the projection is enqueued (_first) once
+    everything that the adapters could be refused for has been looked at."""
+    if _torch is None:
+        _bind()
+    if not {"a", "b"} <= adapters.keys() <= {"a", "b", "scale", "ranks"}:
+        _refuse("adapters: a and b, optionally scale and ranks, are taken")
+    dev = x.get_device()
+    if dev < 0 or x.dim() != 2:
+        _refuse("x: a CUDA tensor [T][cols] is needed")
+    if stream is not None or dev != _current_device():
+        return _elsewhere(_linear_with_adapters, dev, stream, planes, lut, bits, x, rows, y, None,
+                          adapters, ids)
+    T, cols = x.shape
+    px = _flat(x, "x", (T, cols), dev, _bf16_like)
+    if y is None:
+        y = x.new_empty((T, rows), dtype=_f32)
+    py = _flat(y, "y", (T, rows), dev, (_f32,))
+    n_max = planes.numel() * 4 // plane_bytes(rows, cols)
+    return add_adapters(x, adapters["a"], adapters["b"], ids, y, adapters.get("scale"),
+                        adapters.get("ranks"), y, _first=lambda stream: check(lib().pw_linear(
+                            _ptr(planes), _ptr(lut), rows, cols, n_max, bits, px, T, py, stream)))
 
 
 class MoELayer:

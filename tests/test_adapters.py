@@ -326,6 +326,59 @@ def test_norm_projection_adapters_logprobs(gpu, oracle, T):
     assert torch.equal(idx.long(), torch.argsort(z, dim=1, descending=True, stable=True)[:, :5])
 
 
+def projection(gpu, T, cols=128, rows=40, bits=3):
+    import numpy as np
+    from any_precision_weight_pw_b200 import synth
+    rng = np.random.default_rng(T)
+    planes = synth.random_planes(rng, 4, rows, cols)
+    lut = np.sort(rng.normal(0, 0.1, size=(rows, 1 << bits)).astype(np.float16), axis=1)
+    return (gpu.repack_planes(torch.from_numpy(planes.view(np.int32)).cuda(), cols),
+            torch.from_numpy(lut.view(np.int16)).cuda(), bits)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 1100])
+def test_linear_refuses_adapters_before_the_projection(gpu, T):
+    """A refused adapter leaves y as it was."""
+    gen = torch.Generator().manual_seed(T)
+    block = projection(gpu, T)
+    d = make(gen, T, 128, 40, 3, 16)
+    ok = {k: d[k] for k in ("a", "b", "scale", "ranks")}
+    y = torch.full((T, 40), 7.0, device="cuda")
+    for ad, ids in ((ok, None), (ok, d["ids"][:-1]), (ok, d["ids"].long()),
+                    (dict(ok, a=ok["a"][:, :8]), d["ids"]), (dict(ok, scale=ok["scale"][:2]), d["ids"]),
+                    (dict(ok, a=ok["a"][:0], b=ok["b"][:0], scale=None, ranks=None), d["ids"]),
+                    (dict(ok, a=ok["a"].repeat(1, 17, 1), b=ok["b"].repeat(1, 1, 17)), d["ids"]),
+                    (dict(ok, base=y), d["ids"]), (dict(a=ok["a"]), d["ids"]), (None, d["ids"])):
+        with pytest.raises(gpu.PwError):
+            gpu.linear(*block, d["x"], 40, y=y, adapters=ad, adapter_ids=ids)
+    torch.cuda.synchronize()
+    assert (y == 7).all()
+    plain = gpu.linear(*block, d["x"], 40)
+    want = gpu.add_adapters(d["x"], ids=d["ids"], base=plain, **ok)
+    assert torch.equal(gpu.linear(*block, d["x"], 40, y=y, adapters=ok, adapter_ids=d["ids"]), want)
+    assert torch.equal(y, want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = gpu.linear(*block, d["x"], 40, adapters=ok, adapter_ids=d["ids"], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+def test_linear_with_adapters_checks_x_and_y(gpu):
+    gen = torch.Generator().manual_seed(7)
+    block = projection(gpu, 4)
+    d = make(gen, 4, 128, 40, 3, 16)
+    ok = {k: d[k] for k in ("a", "b", "scale", "ranks")}
+    wide = torch.zeros((4, 256), dtype=BF16, device="cuda")
+    for x, y in ((d["x"], torch.empty((4, 40), dtype=BF16, device="cuda")), (d["x"], d["base"][:3]),
+                 (d["x"], torch.empty((4, 44), device="cuda")[:, :40]), (wide[:, :128], None),
+                 (d["x"].float(), None), (d["x"].cpu(), None), (d["x"], d["base"].cpu())):
+        with pytest.raises(gpu.PwError):
+            gpu.linear(*block, x, 40, y=y, adapters=ok, adapter_ids=d["ids"])
+
+
 OK = dict(x=4096, x_ld=64, a=8192, b=16384, ids=32768, ranks=33024, scale=33280, n=2, r=8, T=4, cols=64,
           rows=64, base=65536, base_ld=64, y=131072, y_type=0, y_ld=64, ws=None, ws_bytes=0)
 
