@@ -228,6 +228,7 @@ def plan_release(blocks, target_bytes: int):
 # names are bound once, and tensors made here are not checked again.
 
 _torch = None
+_most = 0x7fffffff  # sizes are passed in 32 bits, which ctypes cuts without a word
 
 
 def _bind() -> None:
@@ -257,6 +258,8 @@ def _refuse(message: str):
 
 def _rows(t, name: str, shape, device: int, types) -> int:
     """Check a [rows][columns] tensor with contiguous rows; its row stride."""
+    if shape[0] > _most or shape[1] > _most:
+        _refuse("%s: shape %s, sizes are below 2^31" % (name, tuple(shape)))
     if t.shape != shape:
         _refuse("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.get_device() != device:
@@ -322,6 +325,8 @@ def add_rms_norm(x, weight, eps: float, residual=None, residual_out=None, y=None
                           scales, y_type, scale_group)
     T, H = shape = x.shape
     x_ld = _rows(x, "x", shape, dev, (0, 1))
+    if scale_group != 0 and scale_group != 128:
+        _refuse("scale_group: 0 (a scale per row) or 128")
     w = _flat(weight, "weight", (H,), dev, (_bf16, _f32, _torch.int16))
     res = r_ld = r_out = ro_ld = r_code = 0
     if residual is not None:
@@ -379,6 +384,8 @@ def token_logprobs(logits, tokens=None, n_top: int = 0, logprob=None, entropy=No
                           top_idx, top_logprob)
     T, V = shape = logits.shape
     ld = _rows(logits, "logits", shape, dev, (0, 1, 2))
+    if n_top > 32:
+        _refuse("n_top: at most 32")
     tok = lp = ti = tl = 0
     if tokens is not None:
         tok = _flat(tokens, "tokens", (T,), dev, (_i32,))
@@ -435,6 +442,8 @@ def add_adapters(x, a, b, ids, base=None, scale=None, ranks=None, y=None, y_type
     T, cols = shape = x.shape
     n, rows, r = b.shape
     x_ld = _rows(x, "x", shape, dev, (1,))
+    if n > _most or r > _most or rows > _most:
+        _refuse("b: shape %s, sizes are below 2^31" % (tuple(b.shape),))
     pa = _flat(a, "a", (n, r, cols), dev, _bf16_like)
     pb = _flat(b, "b", (n, rows, r), dev, _bf16_like)
     pi = _flat(ids, "ids", (T,), dev, (_i32,))

@@ -422,6 +422,17 @@ def test_binding_refuses_cpu_tensors(pw):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32 + 3])
+def test_sizes_past_32_bits_are_refused(gpu, big):
+    gen = torch.Generator().manual_seed(0)
+    d = make(gen, 1, 8, 8, 1, 4)
+    for change, names in ((dict(x=d["x"].expand(big, 8)), "x: shape"),
+                          (dict(b=d["b"][:, :1].expand(1, big, 4)), "b: shape")):
+        with pytest.raises(gpu.PwError, match=names):
+            gpu.add_adapters(**{**d, **change})
+
+
+@pytest.mark.gpu
 def test_binding_refusals(gpu):
     gen = torch.Generator().manual_seed(0)
     d = make(gen, 4, 64, 40, 2, 8)

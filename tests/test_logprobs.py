@@ -249,6 +249,16 @@ def test_binding_refuses_cpu_tensors(pw):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32 + 3])
+def test_sizes_past_32_bits_are_refused(gpu, big):
+    z = torch.zeros((1, 8), device="cuda")
+    with pytest.raises(gpu.PwError):
+        gpu.token_logprobs(z[:, :1].expand(big, 1))
+    with pytest.raises(gpu.PwError):
+        gpu.token_logprobs(z, n_top=big)
+
+
+@pytest.mark.gpu
 def test_binding_refusals(gpu):
     z = torch.zeros((4, 64), device="cuda")
     t = torch.zeros(4, dtype=torch.int32, device="cuda")

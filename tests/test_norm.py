@@ -363,6 +363,24 @@ def test_moe_forward_norm_refusals_and_streams(gpu):
     dev.close()
 
 
+def test_row_checks_know_32_bits(pw):
+    pw._bind()
+    for shape in ((2 ** 31, 1), (2 ** 32 + 3, 1), (1, 2 ** 31)):
+        with pytest.raises(pw.PwError, match="below 2"):
+            pw._rows(torch.zeros(1, 1).expand(shape), "x", shape, -1, (0,))
+    assert pw._rows(torch.zeros(1, 1).expand(2 ** 31 - 1, 1), "x", (2 ** 31 - 1, 1), -1, (0,)) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32 + 3])
+def test_sizes_past_32_bits_are_refused(gpu, big):
+    x, w = torch.zeros((1, 8), dtype=BF16, device="cuda"), torch.ones(8, dtype=BF16, device="cuda")
+    with pytest.raises(gpu.PwError):
+        gpu.add_rms_norm(x[:, :1].expand(big, 1), w[:1], EPS)
+    with pytest.raises(gpu.PwError):
+        gpu.add_rms_norm(x, w, EPS, y_type=E4M3, scale_group=big - big % 2 ** 31)
+
+
 @pytest.mark.gpu
 def test_binding_refusals(gpu):
     x, w = torch.zeros(4, 64, dtype=BF16, device="cuda"), torch.ones(64, dtype=BF16, device="cuda")
