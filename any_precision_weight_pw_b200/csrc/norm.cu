@@ -444,6 +444,19 @@ extern "C" pw_status_t pw_add_rms_norm(const void* d_x, int32_t x_type, int64_t 
   if (x_stride < 0 || residual_stride < 0 || residual_out_stride < 0 || y_stride < 0 ||
       (T > 1 && (y_stride < H || (d_residual_out && residual_out_stride < H))))
     return bad("pw_add_rms_norm: row strides are not negative, and outputs' at least H");
+  // in place a row must lie where the row it replaces lies
+  auto clash = [&](const void* out, int out_type, int64_t out_ld, const void* in, int in_type,
+                   int64_t in_ld) {
+    return out && out == in && (out_type != in_type || (T > 1 && out_ld != in_ld));
+  };
+  if (clash(d_y, y_type, y_stride, d_x, x_type, x_stride) ||
+      clash(d_y, y_type, y_stride, d_residual, residual_type, residual_stride) ||
+      clash(d_residual_out, residual_type, residual_out_stride, d_x, x_type, x_stride) ||
+      clash(d_residual_out, residual_type, residual_out_stride, d_residual, residual_type,
+            residual_stride) ||
+      d_residual_out == d_y)
+    return bad("pw_add_rms_norm: outputs in place have their input's type and stride, and two outputs "
+               "two places");
   if (!aligned_to(d_x, type_bytes(x_type)) || !aligned_to(d_weight, type_bytes(weight_type)) ||
       !aligned_to(d_y, type_bytes(y_type)) ||
       (d_residual && !aligned_to(d_residual, type_bytes(residual_type))) ||

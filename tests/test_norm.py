@@ -132,6 +132,19 @@ def test_in_place_and_repeated_row(gpu, H):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H", [256, 1409])
+@pytest.mark.parametrize("pad", [0, 8])
+def test_outputs_in_the_other_inputs_place(gpu, H, pad):
+    """y in the residual's place, residual_out in x's."""
+    gen = torch.Generator().manual_seed(H + pad)
+    x, res = rows(gen, 70, H, BF16, pad=pad), rows(gen, 70, H, BF16, pad=pad)
+    w = torch.ones(H, dtype=F32, device="cuda")
+    y, _, ro = gpu.add_rms_norm(x, w, EPS, residual=res)
+    gpu.add_rms_norm(x, w, EPS, residual=res, residual_out=x, y=res)
+    assert torch.equal(y, res) and torch.equal(ro, x)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("H", [64, 520, 1409])
 @pytest.mark.parametrize("out,group", [(BF16, 0), (E4M3, 0), (E4M3, 128)])
 def test_zero_huge_and_nonfinite_rows(gpu, H, out, group):
@@ -282,6 +295,18 @@ def test_refusals(pw, change, status):
     assert L.pw_add_rms_norm(*a.values(), None) == status
     if status:
         assert b"pw_add_rms_norm" in L.pw_last_error()
+
+
+@pytest.mark.parametrize("change", [
+    dict(y=4096, y_type=3, scales=131072), dict(y=4096, y_ld=72), dict(y=4096, x_type=0), dict(ro=8192, ro_ld=72),
+    dict(ro=8192, r_ld=0), dict(ro=65536), dict(y=8192, y_ld=72), dict(y=8192, r_type=0),
+    dict(ro=4096, ro_ld=72), dict(ro=4096, r_type=0), dict(y=4096, x_ld=0)])
+def test_refuses_places_that_do_not_match(pw, change):
+    """In place with another stride or type, rows would overwrite rows that are
+    still to be read; two outputs in one place overwrite one another."""
+    L = pw.lib()
+    assert L.pw_add_rms_norm(*{**OK, **change}.values(), None) == 1
+    assert b"in place" in L.pw_last_error()
 
 
 def test_moe_forward_norm_refuses_null_handle(pw):
