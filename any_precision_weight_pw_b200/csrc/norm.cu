@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const NormParams 
           ss = fmaf(h[j][k], h[j][k], ss);
           if constexpr (OUT != kOutBf16) gm[j] = max_nan(gm[j], fabsf(h[j][k] * w[k]));
         }
-        if constexpr (OUT == kOutE4m3Row) mx = max_nan(mx, gm[j]);
+        if constexpr (OUT != kOutBf16) mx = max_nan(mx, gm[j]);
       }
     };
     auto group_max = [&]() {
@@ -282,21 +282,26 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(const NormParams 
     group_max();
     row_reduce(ss, mx, tpr, part[parity]);
     float rstd = 1.0f / sqrtf(fmaf(ss, p.inv_h, p.eps));
-    if (isinf(ss)) {  // the same for the row
-      // The squares left fp32's range: once more on h * f, f = 2^-80, whose
-      // squares cannot (|h| < 2^128, 2^15 columns).  With the mean scaled by f^2,
-      // eps is too: a row that only just overflows has a scaled mean near
-      // 2^-47, far below a usual eps as it stands.  The row then becomes
-      // h / rms, where 1 / rms alone could be subnormal.
-      constexpr float f = 8.271806125530277e-25f;
-      ss = 0.f;
+    // Out of fp32's range, the same for the row: the squares, or (8-bit forms)
+    // the largest |h w|, which only large weights can take there.  The row then
+    // becomes h / rms, where 1 / rms alone could be subnormal.
+    if (isinf(ss) || (OUT != kOutBf16 && isinf(mx))) {
+      float f = 1.0f;
+      if (isinf(ss)) {
+        // once more on h * f, f = 2^-80, whose squares cannot (|h| < 2^128,
+        // 2^15 columns).  With the mean scaled by f^2, eps is too: a row that
+        // only just overflows has a scaled mean near 2^-47, far below a usual
+        // eps as it stands.
+        f = 8.271806125530277e-25f;
+        ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < M; ++j)
+        for (int j = 0; j < M; ++j)
 #pragma unroll
-        for (int k = 0; k < N; ++k) ss = fmaf(h[j][k] * f, h[j][k] * f, ss);
-      parity ^= 1;
-      row_reduce(ss, mx, tpr, part[parity]);
-      rstd = 1.0f / sqrtf(fmaf(ss, p.inv_h, p.eps * f * f));
+          for (int k = 0; k < N; ++k) ss = fmaf(h[j][k] * f, h[j][k] * f, ss);
+        parity ^= 1;
+        row_reduce(ss, mx, tpr, part[parity]);
+        rstd = 1.0f / sqrtf(fmaf(ss, p.inv_h, p.eps * f * f));
+      }
 #pragma unroll
       for (int j = 0; j < M; ++j)
 #pragma unroll

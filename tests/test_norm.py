@@ -132,6 +132,26 @@ def test_in_place_and_repeated_row(gpu, H):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H", [64, 520, 1409, 4096, 9001])
+@pytest.mark.parametrize("out,group", [(BF16, 0), (E4M3, 0), (E4M3, 128)])
+@pytest.mark.parametrize("columns", [1, 300, 1 << 20])
+def test_products_with_large_weights(gpu, H, out, group, columns):
+    """h w leaves fp32 where y does not: the first columns' weights are up to
+    2^100, rows go up to 2^100 (where the squares leave fp32 as well)."""
+    gen = torch.Generator().manual_seed(H + columns)
+    x = (torch.randn((9, H), generator=gen) * 2.0 ** torch.arange(20, 110, 10)[:, None]).cuda()
+    w = torch.randn(H, generator=gen)
+    w[:columns] *= 2.0 ** 100
+    w = w.cuda()
+    y, s, _ = gpu.add_rms_norm(x, w, EPS, y_type=out, scale_group=group)
+    _, want = reference(x, w)
+    if out == BF16:
+        assert ((y.double() - want).abs() <= want.abs() * (2.0 ** -8 + ARITH) + 2.0 ** -133).all()
+    else:
+        check_e4m3(y, s, want, group)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("H", [256, 1409])
 @pytest.mark.parametrize("pad", [0, 8])
 def test_outputs_in_the_other_inputs_place(gpu, H, pad):
