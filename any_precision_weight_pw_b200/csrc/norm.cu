@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -440,7 +441,10 @@ extern "C" pw_status_t pw_add_rms_norm(const void* d_x, int32_t x_type, int64_t 
     return bad("pw_add_rms_norm: y is PW_BF16 or PW_E4M3");
   if (scale_group != 0 && scale_group != kGroup)
     return bad("pw_add_rms_norm: scale_group is 0 (a scale per row) or 128");
-  if (!(eps > 0.f) || !std::isfinite(eps)) return bad("pw_add_rms_norm: eps must be positive and finite");
+  // below 2^-126 the squares that matter beside eps would be subnormal, and the
+  // mean good to a few bits only
+  if (!(eps >= FLT_MIN) || !std::isfinite(eps))
+    return bad("pw_add_rms_norm: eps must be positive (2^-126 at least) and finite");
   if (d_residual_out && !d_residual)
     return bad("pw_add_rms_norm: a residual output needs a residual");
   if (T == 0) return PW_OK;

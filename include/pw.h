@@ -404,7 +404,7 @@ typedef enum { PW_F32 = 0, PW_BF16 = 1, PW_F16 = 2, PW_E4M3 = 3 } pw_dtype_t;
  * rows with H a multiple of 8 are read in 16-byte pieces.  d_residual_out and
  * d_y may be d_residual or d_x, one each, of the same type and stride (refused
  * otherwise); other overlaps are undefined.  T >= 0 (0: nothing is done),
- * 1 <= H <= 32768 (PW_ERR_UNSUPPORTED above), eps > 0. */
+ * 1 <= H <= 32768 (PW_ERR_UNSUPPORTED above), eps >= 2^-126. */
 pw_status_t pw_add_rms_norm(const void* d_x, int32_t x_type, int64_t x_stride,
                             const void* d_residual, int32_t residual_type,
                             int64_t residual_stride, const void* d_weight, int32_t weight_type,

@@ -329,6 +329,30 @@ def test_refuses_places_that_do_not_match(pw, change):
     assert b"in place" in L.pw_last_error()
 
 
+@pytest.mark.parametrize("eps,status", [(2.0 ** -127, 1), (1e-40, 1), (1e-45, 1), (1e-50, 1)])
+def test_refuses_subnormal_eps(pw, eps, status):
+    """The squares beside such an eps would be subnormal, with few bits left."""
+    assert pw.lib().pw_add_rms_norm(*{**OK, "eps": eps}.values(), None) == status
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [8, 1409, 4096])
+@pytest.mark.parametrize("out,group", [(BF16, 0), (E4M3, 0), (E4M3, 128)])
+def test_least_eps(gpu, H, out, group):
+    """Rows around the square root of the least eps, 2^-126: a square is off by
+    2^-150 at most (half a step of the subnormals), 2^-24 of eps."""
+    gen = torch.Generator().manual_seed(H)
+    x = (torch.randn((12, H), generator=gen) * 2.0 ** torch.arange(-72, -48, 2)[:, None]).cuda()
+    w = torch.ones(H, device="cuda")
+    y, s, _ = gpu.add_rms_norm(x, w, 2.0 ** -126, y_type=out, scale_group=group)
+    h = x.double()
+    want = h / torch.sqrt((h * h).mean(1, keepdim=True) + 2.0 ** -126)
+    if out == BF16:
+        assert ((y.double() - want).abs() <= want.abs() * (2.0 ** -8 + ARITH)).all()
+    else:
+        check_e4m3(y, s, want, group)
+
+
 def test_moe_forward_norm_refuses_null_handle(pw):
     assert pw.lib().pw_moe_forward_norm(None, 4096, None, 4096, 1e-6, 1, 4096, None, None, 4096,
                                         None) == 1
