@@ -36,6 +36,7 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <cstdlib>
 #include <mutex>
 #include <type_traits>
 
@@ -70,6 +71,9 @@ struct AdapterParams {
   int r32;         // max_rank in whole 32s
   int tile_rows;   // many tokens: rows of an expand tile
   int split;       // and blocks of a shrink cluster
+  unsigned long long wait_ns;  // limit of a wait
+  int stall_tile;  // test switch: this tile's products are not issued (-1: none;
+                   // in expand -2 - tile)
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -634,9 +638,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-// Wait for an mbarrier phase, two seconds at most; a wait that gives up makes
-// the block's later ones give up at once.
-__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+// Wait for an mbarrier phase, limit_ns at most; a wait that gives up makes the
+// block's later ones give up at once.
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                          unsigned long long limit_ns) {
   unsigned long long t0 = 0, t = 0;
   while (true) {
     uint32_t ok;
@@ -649,7 +654,7 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatil
     if (ok || *gave_up) return;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     if (t0 == 0) t0 = t;
-    if (t - t0 > 2000000000ull) {
+    if (t - t0 > limit_ns) {
       *gave_up = 1;
       return;
     }
@@ -666,6 +671,22 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
         "=r"(u[14]), "=r"(u[15])
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// What is written where a wait gave up.
+__device__ __forceinline__ float lost_value() { return __int_as_float(0x7fffffff); }
+
+// Before tensor memory goes back after a wait that gave up: the products still
+// in flight, waited for once more (all threads).
+__device__ __forceinline__ void drain_products(uint32_t bar, unsigned long long limit_ns) {
+  if (threadIdx.x >= 32) return;
+  if (elect_one())
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+  __syncwarp();
+  int again = 0;
+  mbar_wait(bar, 0, &again, limit_ns);
 }
 
 constexpr int kShrinkStages = 3;
@@ -692,7 +713,7 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
   __shared__ __align__(16) int s_key[kWindow];
   __shared__ int s_tok[kWindow], s_sid[kWindow];
   __shared__ TileInfo s_info;
-  __shared__ __align__(8) uint64_t s_bar[2];  // products of even and odd steps
+  __shared__ __align__(8) uint64_t s_bar[3];  // products of even and odd steps; the end, after a lost wait
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up;
   const uint32_t sm = (smem_u32(smem) + 1023) & ~1023u;
@@ -713,6 +734,7 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
   if (tid == 0) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar));
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar + 8));
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar + 16));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_gave_up = 0;
   }
@@ -835,7 +857,7 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
   // Steps so far.  A step's wait comes after the next one's products have been
   // issued, hence two barriers: one would be two phases ahead of it.
   uint32_t n_done = 0;
-  auto wait_step = [&](uint32_t n) { mbar_wait(bar + (n & 1) * 8, n >> 1 & 1, &s_gave_up); };
+  auto wait_step = [&](uint32_t n) { mbar_wait(bar + (n & 1) * 8, n >> 1 & 1, &s_gave_up, p.wait_ns); };
   int stage = 0;
   bool sums_read = false;  // an arrive without its wait: this block has read its sums
   for (int g0 = 0; g0 < n_segments; g0 += 2) {
@@ -853,7 +875,7 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();  // the step is there
-        if (warp == 0) {
+        if (warp == 0 && cl != p.stall_tile) {
           tc_fence_after();
           if (elect_one()) {
             const uint32_t at = sm + stage * kShrinkStage;
@@ -902,6 +924,10 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
               for (int e = 0; e < 32; ++e) v[e] = mine ? v[e] + u[e] : v[e];
             }
           }
+          if (*static_cast<volatile int*>(&s_gave_up)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = lost_value();
+          }
           if (t < w.len)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -939,6 +965,7 @@ __global__ void __launch_bounds__(kAdThreads, 2) shrink_kernel(const AdapterPara
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   tc_fence_before();
   __syncthreads();
+  if (s_gave_up) drain_products(bar + 16, p.wait_ns);
   tc_fence_after();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
@@ -970,7 +997,7 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ TileInfo s_info;
   __shared__ int64_t s_base[kTileTokens], s_y[kTileTokens];  // byte offsets of the segment's tokens
-  __shared__ __align__(8) uint64_t s_bar;
+  __shared__ __align__(8) uint64_t s_bar[2];  // products; the end, after a lost wait
   __shared__ uint32_t s_tmem;
   __shared__ int s_gave_up;
   const uint32_t sm = (smem_u32(smem) + 1023) & ~1023u;  // v: [term][step], then the stages of B
@@ -984,10 +1011,11 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
   const bool in_place = p.base == p.y;
   const uint8_t* ws = p.ws + tile * tile_bytes(kTerms, p.v_ld);
   const uint16_t* vt = reinterpret_cast<const uint16_t*>(ws + sizeof(TileInfo));
-  const uint32_t bar = smem_u32(&s_bar);
+  const uint32_t bar = smem_u32(s_bar);
   pdl_wait();
   if (tid == 0) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar));
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar + 8));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_gave_up = 0;
   }
@@ -1148,7 +1176,7 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncthreads();  // this step's B is there, the accumulators have been read
           const int n_k = min((rank - r0 + 15) / 16, 4);  // MMA steps of a term
-          if (warp == 0 && n_k > 0) {
+          if (warp == 0 && n_k > 0 && -2 - p.stall_tile != tile) {
             tc_fence_after();
             if (elect_one()) {
               const uint64_t b = operand_desc(sm + st0 + stage * kBTile);
@@ -1171,7 +1199,7 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
           stage = stage + 1 == STAGES ? 0 : stage + 1;
           issue();  // into the stage of the step before, whose products are done
           if (n_k > 0) {
-            mbar_wait(bar, phase, &s_gave_up);
+            mbar_wait(bar, phase, &s_gave_up, p.wait_ns);
             phase ^= 1;
           }
         }
@@ -1229,12 +1257,32 @@ __global__ void __launch_bounds__(kAdThreads, NC == 1 ? 2 : 1) expand_kernel(con
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   tc_fence_before();
   __syncthreads();
+  if (s_gave_up) {  // NaN over what this block has written for tokens with an adapter
+    for (int i = 0; i < n_segments; ++i) {
+      const Piece sg = s_info.segment[i];
+      if (sg.rank == 0) continue;
+      for (int t = sg.start; t < sg.start + sg.len; ++t)
+        for (int r = tid; r < rows; r += kAdThreads) {
+          E* at = static_cast<E*>(p.y) + s_info.tok[t] * p.y_ld + first + r;
+          if constexpr (F32)
+            *at = lost_value();
+          else
+            *at = bf16_bits(lost_value());
+        }
+    }
+    drain_products(bar + 8, p.wait_ns);
+  }
   tc_fence_after();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kExpandCols));
 }
 
 // ---- host ------------------------------------------------------------------
+
+int env_int(const char* name, int otherwise) {
+  const char* v = std::getenv(name);
+  return v ? std::atoi(v) : otherwise;
+}
 
 // The kernel's dynamic shared memory limit, once per device.
 template <auto kernel>
@@ -1428,6 +1476,10 @@ extern "C" pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const 
     e = f32 ? (vec ? launch_few<true, true>(p, s) : launch_few<true, false>(p, s))
             : (vec ? launch_few<false, true>(p, s) : launch_few<false, false>(p, s));
   } else {
+    // waits are limited to two seconds, or as the test switches say
+    const int wait_us = env_int("PW_TEST_WAIT_US", 0);
+    p.wait_ns = wait_us > 0 ? wait_us * 1000ull : 2000000000ull;
+    p.stall_tile = env_int("PW_TEST_STALL_TILE", -1);
     // columns split while the blocks fit the GPU twice over
     p.split = kAdCluster;
     while (p.split > 1 && tiles * p.split > 2 * n_sm) p.split /= 2;

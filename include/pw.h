@@ -80,7 +80,9 @@
  *   failure-detection test PW_TEST_WAIT_US=n (device wait limit, default 2 s)
  *   with PW_TEST_STALL_GROUP=g (expert g's down items wait for a gate/up count
  *   that never arrives, so the bounded wait runs out and the forward reports
- *   PW_ERR_TIMEOUT through pw_check_device_error).
+ *   PW_ERR_TIMEOUT through pw_check_device_error), or, for pw_adapters above
+ *   1024 tokens, PW_TEST_STALL_TILE=t (the products of ordered tokens 64 t to
+ *   64 t + 63 are not issued in the first kernel; -2 - t: in the second).
  */
 #ifndef PW_H_
 #define PW_H_
@@ -453,8 +455,8 @@ pw_status_t pw_token_logprobs(const void* d_logits, int32_t logits_type, int64_t
  * workspace_bytes >= pw_adapters_workspace_bytes (0 up to 1024 tokens, then
  * NULL is accepted), 16-byte aligned, used by this call alone until its work
  * is done; its contents need not be set or kept.  cols and rows up to 2^28
- * (PW_ERR_UNSUPPORTED above).  Device waits are bounded as pw_linear's: one
- * that gives up leaves d_y unspecified without a report. */
+ * (PW_ERR_UNSUPPORTED above).  Device waits are bounded to two seconds; where
+ * one gives up, those of its up to 64 tokens that have an adapter get NaN. */
 #define PW_MAX_ADAPTER_RANK 256
 #define PW_MAX_ADAPTERS 4194303
 pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const uint16_t* d_a,

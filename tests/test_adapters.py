@@ -326,6 +326,32 @@ def test_norm_projection_adapters_logprobs(gpu, oracle, T):
     assert torch.equal(idx.long(), torch.argsort(z, dim=1, descending=True, stable=True)[:, :5])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols,rows,r,y", [(264, 72, 16, F32), (64, 300, 72, F32), (1409, 130, 64, BF16)])
+@pytest.mark.parametrize("kernel", ["shrink", "expand"])
+@pytest.mark.parametrize("tile", [0, 5, 32])
+def test_a_wait_that_gives_up_leaves_nan(gpu, monkeypatch, cols, rows, r, y, kernel, tile):
+    """Failure detection without a fault: the test switches leave the products
+    of one tile out, so the waits for them run out (5 ms).  Its tokens with an
+    adapter get NaN, every other token what it always gets, and the next call
+    is as ever."""
+    gen = torch.Generator().manual_seed(tile)
+    T = 2100
+    d = make(gen, T, cols, rows, 3, r, y, ranks=False)
+    d["ids"] = (torch.arange(T, device="cuda") // 50 % 4 - 1).int()     # long runs: order is kept
+    want = gpu.add_adapters(**d)
+    torch.cuda.synchronize()
+    monkeypatch.setenv("PW_TEST_WAIT_US", "5000")
+    monkeypatch.setenv("PW_TEST_STALL_TILE", str(tile if kernel == "shrink" else -2 - tile))
+    got = gpu.add_adapters(**d)
+    torch.cuda.synchronize()
+    monkeypatch.undo()
+    lost = (torch.arange(T, device="cuda") // 64 == tile) & (d["ids"] >= 0)
+    assert lost.any() and not lost.all()
+    assert got[lost].isnan().all() and torch.equal(got[~lost], want[~lost])
+    assert torch.equal(gpu.add_adapters(**d), want)
+
+
 def projection(gpu, T, cols=128, rows=40, bits=3):
     import numpy as np
     from any_precision_weight_pw_b200 import synth
