@@ -400,7 +400,8 @@ typedef enum { PW_F32 = 0, PW_BF16 = 1, PW_F16 = 2, PW_E4M3 = 3 } pw_dtype_t;
  * y_type PW_E4M3: d_y holds q = e4m3(y / s) with s = max(max|y| / 448, 2^-126)
  * over the row (scale_group 0, d_scales fp32 [T]) or over each 128 columns of
  * it (scale_group 128, d_scales fp32 [T][ceil(H / 128)]); y ~ s * q, and a row
- * (group) holding NaN has s = NaN.
+ * (group) holding NaN has s = NaN.  The quotient is taken as y * (1 / s)
+ * in fp32: one next to the border of two e4m3 values may fall to either.
  *   Strides count elements between rows (inputs: 0 repeats one row); rows are
  * contiguous.  Buffers need only their elements' alignment; 16-byte aligned
  * rows with H a multiple of 8 are read in 16-byte pieces.  d_residual_out and
@@ -450,13 +451,15 @@ pw_status_t pw_token_logprobs(const void* d_logits, int32_t logits_type, int64_t
  * strides count elements between rows; rows, A and B are contiguous.  Buffers
  * need only their elements' alignment; 16-byte aligned rows are read in
  * 16-byte pieces.  Accumulation is fp32, A_a x_t enters the second product
- * with 24 (y fp32) or 16 (y bf16) significant bits.  T >= 0,
- * 1 <= max_rank <= PW_MAX_ADAPTER_RANK.  d_workspace: device memory of
- * workspace_bytes >= pw_adapters_workspace_bytes (0 up to 1024 tokens, then
- * NULL is accepted), 16-byte aligned, used by this call alone until its work
- * is done; its contents need not be set or kept.  cols and rows up to 2^28
- * (PW_ERR_UNSUPPORTED above).  Device waits are bounded to two seconds; where
- * one gives up, those of its up to 64 tokens that have an adapter get NaN. */
+ * with 24 (y fp32) or 16 (y bf16) significant bits, as two or three terms: an
+ * infinite element of B can make its outputs NaN where one product would be
+ * infinite.  T >= 0, 1 <= max_rank <= PW_MAX_ADAPTER_RANK.  d_workspace:
+ * device memory of workspace_bytes >= pw_adapters_workspace_bytes (0 up to
+ * 1024 tokens, then NULL is accepted), 16-byte aligned, used by this call alone
+ * until its work is done; its contents need not be set or kept.  cols and rows
+ * up to 2^28 (PW_ERR_UNSUPPORTED above).  Device waits are bounded to two
+ * seconds; where one gives up, those of its up to 64 tokens that have an
+ * adapter get NaN. */
 #define PW_MAX_ADAPTER_RANK 256
 #define PW_MAX_ADAPTERS 4194303
 pw_status_t pw_adapters(const uint16_t* d_x, int64_t x_stride, const uint16_t* d_a,
@@ -470,7 +473,7 @@ int64_t pw_adapters_workspace_bytes(int32_t T, int32_t max_rank, int32_t y_type)
 /* pw_moe_forward of a pre-norm block: y = MoE(x') with x' the bf16 y of
  * pw_add_rms_norm(x, residual, norm_w, eps); residual_out as there.  d_x bf16
  * [T][H], d_residual bf16 [T][H] or NULL, d_norm_w bf16 [H], d_residual_out
- * bf16 [T][H] or NULL (may be d_residual), all contiguous and 16-byte
+ * bf16 [T][H] or NULL (may be d_residual, not d_y), all contiguous and 16-byte
  * aligned.  x' is kept in the handle's workspace.  d_y may be d_x. */
 pw_status_t pw_moe_forward_norm(pw_moe_t* h, const uint16_t* d_x, const uint16_t* d_residual,
                                 const uint16_t* d_norm_w, float eps, int32_t T,

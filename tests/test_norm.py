@@ -91,6 +91,26 @@ def test_matches_float64(gpu, T, H, xt, rt, wt, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [(64, 4096), (2048, 4096), (300, 1409)])
+@pytest.mark.parametrize("group", [0, 128])
+def test_e4m3_is_the_nearest_but_at_borders(gpu, T, H, group):
+    """q is e4m3(y / s) of the float64 y: only a quotient within the arithmetic's
+    error of the border between two e4m3 values may fall to its other side."""
+    gen = torch.Generator().manual_seed(T + H)
+    x, res = rows(gen, T, H, BF16), rows(gen, T, H, BF16, 4.0)
+    w = (torch.randn(H, generator=gen) * 0.2 + 1).to(BF16).cuda()
+    q, s, _ = gpu.add_rms_norm(x, w, EPS, residual=res, y_type=E4M3, scale_group=group)
+    _, y = reference(x, w, res)
+    full = s.double().repeat_interleave(group or H, 1)[:, :H]
+    exact = y / full
+    low, high = ((exact * (1 + d)).clamp(-448, 448).float().to(E4M3).float() for d in (-ARITH, ARITH))
+    got = q.float()
+    assert ((got == low) | (got == high)).all()
+    # borders are 2^-4 and more apart, so few quotients are that close to one
+    assert (got != exact.clamp(-448, 448).float().to(E4M3).float()).double().mean() <= 2 * ARITH * 2 ** 4
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("pad", [3, 8])
 @pytest.mark.parametrize("out,group", [(BF16, 0), (E4M3, 0), (E4M3, 128)])
 def test_strided_rows_and_untouched_gaps(gpu, pad, out, group):
