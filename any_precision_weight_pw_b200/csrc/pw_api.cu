@@ -960,6 +960,8 @@ pw_status_t pw_moe_forward_norm(pw_moe_t* h, const uint16_t* d_x, const uint16_t
   if (!aligned16(d_x) || !aligned16(d_residual) || !aligned16(d_norm_w) ||
       !aligned16(d_residual_out) || !aligned16(d_router_w) || !aligned16(d_y))
     return fail(PW_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
+  if (d_residual_out && d_residual_out == d_y)
+    return fail(PW_ERR_INVALID_ARG, "the residual output and y need two places");
   // the norm's output takes the place pw_moe_forward_host copies its rows to
   const int32_t H = h->cfg.hidden;
   const pw_status_t st = pw_add_rms_norm(d_x, PW_BF16, H, d_residual, PW_BF16, H, d_norm_w, PW_BF16,

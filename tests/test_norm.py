@@ -417,6 +417,25 @@ def test_binding_refuses_cpu_tensors(pw):
 
 
 @pytest.mark.gpu
+def test_moe_forward_norm_outputs_need_two_places(gpu):
+    from any_precision_weight_pw_b200 import synth
+    layer = synth.Layer(synth.WORKLOADS["tiny_h256_f512_e8k2"], seed=0)
+    dev = gpu.upload_synth_layer(layer, max_tokens=16)
+    H = layer.wl.hidden
+    x, w = torch.ones((3, H), dtype=BF16, device="cuda"), torch.ones(H, dtype=BF16, device="cuda")
+    wr, out = torch.from_numpy(layer.router_w).cuda(), torch.full((3, H), 7.0, dtype=BF16, device="cuda")
+    with pytest.raises(gpu.PwError, match="two places"):
+        dev.forward_norm(x, w, EPS, wr, residual=x, residual_out=out, y=out)
+    torch.cuda.synchronize()
+    assert (out == 7).all()
+    want = dev.forward_norm(x, w, EPS, wr, residual=x)
+    x2 = x.clone()
+    assert dev.forward_norm(x2, w, EPS, wr, residual=x, residual_out=out, y=x2)[0] is x2
+    assert torch.equal(x2, want[0]) and torch.equal(out, want[1])
+    dev.close()
+
+
+@pytest.mark.gpu
 def test_moe_forward_norm_refusals_and_streams(gpu):
     """Types, devices and layouts are refused before anything runs; on another
     stream the outputs are the same."""
