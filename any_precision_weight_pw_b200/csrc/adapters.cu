@@ -32,7 +32,9 @@
 //
 // Precision.  v is split into bf16 terms (v = hi + mid + lo, 24 bits; two
 // terms, 16 bits, when y is bf16 and rounds to 8), each multiplied with B
-// exactly; sums are fp32.
+// exactly; sums are fp32.  The two terms of a bf16 y save a third of the
+// products and of v's shared memory; what they leave out, 2^-17 |B| |v|, shows
+// only where base and B v cancel to less than 2^-8 of them.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -984,7 +986,7 @@ constexpr int kExpandStages = 3;
 // values of one adapter never meet another's tokens.)  The product is taken
 // this way round because tensor memory hands each lane one row of D: a warp's
 // 32 lanes then hold 32 neighbouring rows of W for a token, and base and y move
-// in whole 128-byte lines at any alignment.  B is copied to shared memory
+// in runs of 128 bytes (fp32; bf16 64) at any alignment.  B is copied to shared memory
 // asynchronously in steps of 64 ranks, STAGES - 1 steps ahead; base is loaded
 // 128 rows ahead into registers.
 // NC: 64-rank steps at most.  VEC: 16-byte copies of B are legal.
