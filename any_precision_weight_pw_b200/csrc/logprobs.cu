@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kLpThreads, B) logprob_kernel(const LogprobPar
     const unsigned long long bound = s_bound;
     // A logit reaches the bound if it is larger, or equal and not behind the
     // bound's vector.
-    const uint32_t last = bound ? static_cast<uint32_t>(~(key_index(bound) + N - 1)) : 0u;
+    const uint32_t last = bound ? ~(static_cast<uint32_t>(key_index(bound)) + N - 1) : 0u;
     const unsigned long long reach = (bound & 0xffffffff00000000ull) | last;
     if (key != 0 && key >= bound) s_thread[atomicAdd(&s_threads, 1)] = static_cast<uint16_t>(tid);
     __syncthreads();

@@ -225,6 +225,21 @@ def test_offsets_past_32_bits(gpu):
     check(gpu.token_logprobs(z, tokens, n_top=5), reference(z, tokens, 5), V)
 
 
+@pytest.mark.gpu
+def test_longest_row(gpu):
+    """2^31 - 1 logits: indices up to the last one, ties among the last vectors."""
+    V = 2 ** 31 - 1
+    z = torch.full((1, V), -1.0, dtype=BF16, device="cuda")
+    at = [V - 1, V - 2, V - 9, V - 8, 12345, V - 17, 0]
+    z[0, at] = 2.0
+    z[0, V - 3] = 3.0
+    tokens = torch.tensor([V - 1], dtype=torch.int32, device="cuda")
+    lp, _, idx, top = gpu.token_logprobs(z, tokens, n_top=10)
+    rest = [i for i in range(20) if i not in at][:2]
+    assert idx[0].tolist() == [V - 3] + sorted(at) + rest
+    assert lp[0] == top[0, 1] and (top[0, 1:8] == lp[0]).all()
+
+
 OK = dict(z=4096, type=0, ld=10, T=2, V=10, tokens=8192, n_top=2, lp=8704, ent=9216, idx=9728,
           top=10240)
 
